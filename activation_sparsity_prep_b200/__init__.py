@@ -11,7 +11,10 @@ the dequantised backbone) feeds a sparse FP4 GEMM and a dense FP4 GEMM that
 share one FP4 weight payload.  For a SwiGLU MLP the gate+up linear can apply
 the gate in its epilogue (linear_swiglu / moe_linear_swiglu) and hand max |H|
 to the down projection's prepare (prepare_amax), which then skips its own
-amax pass.
+amax pass.  Around them stand routing to experts (moe_route, moe_dispatch,
+moe_combine), the residual addition with its norms (residual_norm) and linears
+in 8-bit integers (quantize_weight_int8, prepare_int8, linear_int8), in
+``ops.py``.
 """
 from __future__ import annotations
 
@@ -26,7 +29,9 @@ __all__ = [
     "prepare_workspace_bytes", "Weight", "Prepared", "quantize_weight",
     "prepare", "prepare_layernorm", "prepare_amax", "prepare_noalloc", "linear",
     "linear_swiglu", "interleave_gate_up", "moe_linear", "moe_linear_swiglu",
-    "moe_workspace_bytes", "selftest_wait_timeout", "selftest_prepare_timeout", "last_device_status",
+    "moe_workspace_bytes", "Routing", "moe_route", "moe_dispatch", "moe_combine", "residual_norm",
+    "PreparedInt8", "WeightInt8", "prepare_int8", "quantize_weight_int8", "linear_int8",
+    "selftest_wait_timeout", "selftest_prepare_timeout", "last_device_status",
 ]
 
 NVFP4, MXFP4 = 0, 1
@@ -581,3 +586,16 @@ def selftest_prepare_timeout(X, limit_us: int = 10000, stream=None) -> Prepared:
 def last_device_status(stream=None) -> int:
     """Synchronise and return (then clear) the device status word."""
     return int(load_sharq_ops().sharq_last_device_status(_stream(stream)))
+
+
+_OPS = ("Routing", "moe_route", "moe_dispatch", "moe_combine", "residual_norm", "PreparedInt8", "WeightInt8",
+        "prepare_int8", "quantize_weight_int8", "linear_int8")
+
+
+def __getattr__(name):
+    """The operators of ops.py, which needs torch at import, on first use."""
+    if name in _OPS:
+        from . import ops
+        globals().update({n: getattr(ops, n) for n in _OPS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

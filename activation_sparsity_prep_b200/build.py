@@ -13,8 +13,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsharq.so")
-SOURCES = ["abi.cu", "prepare.cu", "linear.cu", "noalloc.cu", "selftest.cu"]
-HEADERS = ["common.cuh", "sharq_internal.h"]
+SOURCES = ["abi.cu", "prepare.cu", "linear.cu", "noalloc.cu", "selftest.cu",
+           "abi_ops.cu", "norm.cu", "route.cu", "int8.cu"]
+HEADERS = ["common.cuh", "sharq_internal.h", "ops_common.cuh", "ops_internal.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -1,0 +1,446 @@
+"""The rest of a layer around its linears: routing to experts and back, the
+residual addition with its norms, and linears in 8-bit integers.
+
+Python binding of the second half of ``include/sharq.h``, where the formulas
+stand.  As in the rest of the package every call checks its tensors first
+(ValueError, nothing enqueued), returns without synchronising, and has no CPU
+fallback.  A call runs on the device of its tensors; with ``stream`` it runs
+there, and what it allocates belongs to that stream.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+from dataclasses import dataclass
+from typing import Optional, Tuple
+
+import torch
+
+_P, _I, _I64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+
+
+class _Routing(ctypes.Structure):
+    _fields_ = [("ids", _P), ("weights", _P), ("row_index", _P), ("offsets", _P), ("position", _P),
+                ("T", _I64), ("k", _I), ("E", _I)]
+
+
+class _RouteOptions(ctypes.Structure):
+    _fields_ = [("score", _I), ("groups", _I), ("topk_groups", _I), ("group_score", _I),
+                ("renormalize", _I), ("scale", _F)]
+
+
+class _RowsInt8(ctypes.Structure):
+    _fields_ = [("codes", _P), ("scales", _P), ("M", _I64), ("K", _I)]
+
+
+class _WeightInt8(ctypes.Structure):
+    _fields_ = [("codes", _P), ("scales", _P), ("N", _I), ("K", _I)]
+
+
+class _ResidualNorm(ctypes.Structure):
+    _fields_ = ([(n, _P) for n in ("x", "h", "post_gamma", "gate", "gamma", "beta", "scale", "shift", "out_x", "y")]
+                + [("q", ctypes.POINTER(_RowsInt8))]
+                + [(n, _I64) for n in ("ld_x", "ld_h", "ld_gate", "ld_scale", "ld_shift", "ld_out", "M", "G")]
+                + [(n, _I) for n in ("K", "norm", "x_is_fp32", "h_is_fp32", "norm_is_fp32", "mod_is_fp32")]
+                + [("alpha", _F), ("eps", _F)])
+
+
+def _declare(L: ctypes.CDLL) -> None:
+    """Argument types of the entry points this module calls."""
+    R = ctypes.POINTER(_Routing)
+    for name, args in (
+            ("sharq_moe_route", [_P, _I64, _I, _P, ctypes.POINTER(_RouteOptions), R, _P]),
+            ("sharq_moe_dispatch", [R, _P]),
+            ("sharq_moe_combine", [_P, _I, _I64, _I, _P, _P, _I64, _I, _P, _P, _I, _P]),
+            ("sharq_residual_norm", [ctypes.POINTER(_ResidualNorm), _P]),
+            ("sharq_prepare_int8", [_P, _P, _F, ctypes.POINTER(_RowsInt8), _P]),
+            ("sharq_quantize_weight_int8", [_P, ctypes.POINTER(_WeightInt8), _P]),
+            ("sharq_linear_int8", [ctypes.POINTER(_RowsInt8), ctypes.POINTER(_WeightInt8), _P, _I, _P, _I, _P])):
+        fn = getattr(L, name)
+        fn.argtypes, fn.restype = args, _I
+
+
+_lib = None
+
+
+def _call(name: str, *args) -> None:
+    global _lib
+    from . import SharqError, load_sharq_ops
+    if _lib is None:
+        L = load_sharq_ops()
+        _declare(L)
+        _lib = L
+    st = getattr(_lib, name)(*args)
+    if st != 0:
+        raise SharqError(name, st)
+
+
+def _stream(dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _need(cond: bool, msg: str) -> None:
+    if not cond:
+        raise ValueError(msg)
+
+
+def _placed(fn):
+    """Run a call on its first tensor's device and, when given, on `stream`:
+    kernels, allocations and frees then all belong to that stream."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        t = first.codes if isinstance(first, (PreparedInt8, WeightInt8)) else first
+        _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{fn.__name__} needs CUDA tensors")
+        if stream is None and t.device.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        _need(stream is None or stream.device == t.device, f"the stream is on {stream and stream.device}, "
+              f"the tensors on {t.device}")
+        with torch.cuda.device(t.device), torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
+    return call
+
+
+_BF16_FP32 = (torch.bfloat16, torch.float32)
+
+
+def _flat(name: str, t, shape: Tuple[int, ...], dtypes, dev, align: int = 16):
+    """t: a contiguous tensor of `shape` and one of `dtypes` on `dev`."""
+    _need(isinstance(t, torch.Tensor), f"{name} is required")
+    _need(tuple(t.shape) == shape, f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    _need(t.dtype in dtypes, f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    _need(t.device == dev, f"{name} is on {t.device}, expected {dev}")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
+    _need(t.data_ptr() % align == 0, f"{name} must start on a {align}-byte boundary")
+
+
+def _rows(name: str, t, shape: Tuple[int, int], dtypes, dev, align: int = 16) -> int:
+    """t: [rows, K] with unit stride along K, any row stride of whole
+    `align` bytes; returns that stride in elements."""
+    _need(isinstance(t, torch.Tensor), f"{name} is required")
+    _need(tuple(t.shape) == shape, f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    _need(t.dtype in dtypes, f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    _need(t.device == dev, f"{name} is on {t.device}, expected {dev}")
+    _need(shape[1] == 1 or t.stride(1) == 1, f"{name} must have unit stride along its rows")
+    ld = t.stride(0) if shape[0] > 1 else shape[1]
+    _need(ld >= shape[1], f"{name} must not overlap itself (row stride {ld})")
+    _need(t.data_ptr() % align == 0 and (ld * t.element_size()) % align == 0,
+          f"every row of {name} must start on a {align}-byte boundary")
+    return ld
+
+
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+# ------------------------------------------------------------- routing --
+
+_SCORE = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORE = {"max": 0, "top2": 1}
+_I32 = (torch.int32,)
+_FP32 = (torch.float32,)
+
+
+@dataclass
+class Routing:
+    """Each token's experts and the order a grouped linear takes them in."""
+    ids: "object"            # int32 [T, k], -1 for none
+    weights: "object"        # fp32 [T, k] (None when built by moe_dispatch)
+    row_index: "object"      # int32 [T * k], token of each dispatched row
+    offsets: "object"        # int32 [E + 1]
+    position: "object"       # int32 [T, k], dispatched row of each choice, -1 for none
+
+    @staticmethod
+    def empty(T: int, k: int, E: int, device="cuda") -> "Routing":
+        n = T * k
+        # one allocation; the parts start on 16-byte boundaries
+        at = [0]
+        for size in (n, n, n, E + 1, n):
+            at.append(at[-1] + (size + 3) // 4 * 4)
+        b = torch.empty((at[-1],), dtype=torch.int32, device=device)
+        part = [b[o:o + s] for o, s in zip(at, (n, n, n, E + 1, n))]
+        return Routing(part[0].view(T, k), part[1].view(torch.float32).view(T, k), part[2], part[3], part[4].view(T, k))
+
+
+def _check_routing(r: Routing, T: int, k: int, E: int, dev) -> None:
+    _flat("out.ids", r.ids, (T, k), _I32, dev, 4)
+    _flat("out.weights", r.weights, (T, k), _FP32, dev, 4)
+    _flat("out.row_index", r.row_index, (T * k,), _I32, dev, 4)
+    _flat("out.offsets", r.offsets, (E + 1,), _I32, dev, 4)
+    _flat("out.position", r.position, (T, k), _I32, dev, 4)
+
+
+@_placed
+def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+              group_score: str = "max", renormalize: bool = True, scale: float = 1.0,
+              out: Optional[Routing] = None) -> Routing:
+    """Choose k experts for each token and build the dispatch order.
+
+    logits: [T, E] bf16 or fp32 (any row stride), -inf or NaN where an expert
+    is masked; score: "softmax" or "sigmoid"; bias: fp32 [E], added for the
+    choice only; groups / topk_groups / group_score ("max" or "top2"): keep
+    the best groups of neighbouring experts first.  A token with fewer than k
+    experts left has ids of -1 and weights of 0 behind them.  The result's
+    row_index and offsets go to moe_linear, position and weights to
+    moe_combine."""
+    _need(logits.dim() == 2, "logits must be a 2-D tensor [T, E]")
+    T, E = logits.shape
+    dev = logits.device
+    _need(score in _SCORE, f"score is {score!r}, expected 'softmax' or 'sigmoid'")
+    _need(group_score in _GROUP_SCORE, f"group_score is {group_score!r}, expected 'max' or 'top2'")
+    _need(1 <= E <= 512, f"E={E} experts, expected 1 to 512")
+    _need(1 <= groups <= 32 and E % groups == 0, f"groups={groups} must divide E={E} and be at most 32")
+    _need(1 <= topk_groups <= groups, f"topk_groups={topk_groups}, expected 1 to {groups}")
+    _need(1 <= k <= min(32, E // groups * topk_groups),
+          f"k={k}, expected 1 to {min(32, E // groups * topk_groups)}")
+    _need(T * k < 2 ** 31, f"T * k = {T * k} choices, expected below 2^31")
+    ld = _rows("logits", logits, (T, E), _BF16_FP32, dev, 2)
+    if bias is not None:
+        _flat("bias", bias, (E,), _FP32, dev, 4)
+    if out is not None:
+        _check_routing(out, T, k, E, dev)
+    r = out if out is not None else Routing.empty(T, k, E, dev)
+    opt = _RouteOptions(_SCORE[score], groups, topk_groups, _GROUP_SCORE[group_score], 1 if renormalize else 0, scale)
+    c = _Routing(r.ids.data_ptr(), r.weights.data_ptr(), r.row_index.data_ptr(), r.offsets.data_ptr(),
+                 r.position.data_ptr(), T, k, E)
+    _call("sharq_moe_route", logits.data_ptr(), ld, 1 if logits.dtype == torch.float32 else 0, _ptr(bias),
+          ctypes.byref(opt), ctypes.byref(c), _stream(dev))
+    return r
+
+
+@_placed
+def moe_dispatch(ids, E: int) -> Routing:
+    """Dispatch order of given expert ids (int32 [T, k]; outside 0 .. E-1:
+    dropped), as moe_route builds it.  The result's weights are None."""
+    _need(ids.dim() == 2, "ids must be a 2-D tensor [T, k]")
+    T, k = ids.shape
+    dev = ids.device
+    _need(1 <= E <= 512, f"E={E} experts, expected 1 to 512")
+    _need(k >= 1 and T * k < 2 ** 31, f"T * k = {T * k} choices of k={k}, expected k >= 1 and below 2^31")
+    _flat("ids", ids, (T, k), _I32, dev, 4)
+    i32 = dict(dtype=torch.int32, device=dev)
+    r = Routing(ids, None, torch.empty((T * k,), **i32), torch.empty((E + 1,), **i32), torch.empty((T, k), **i32))
+    c = _Routing(ids.data_ptr(), None, r.row_index.data_ptr(), r.offsets.data_ptr(), r.position.data_ptr(), T, k, E)
+    _call("sharq_moe_dispatch", ctypes.byref(c), _stream(dev))
+    return r
+
+
+@_placed
+def moe_combine(Y, position, weights, residual=None, out=None):
+    """Expert outputs back to the tokens: sum_j weights[t, j] *
+    Y[position[t, j]] (+ residual[t]).  Y: [rows, N] in dispatch order, bf16
+    or fp32; position int32 and weights fp32 [T, k]; residual [T, N] bf16 or
+    fp32, which is then the result's type (else Y's).  out may be residual."""
+    _need(Y.dim() == 2, "Y must be a 2-D tensor [rows, N]")
+    rows, N = Y.shape
+    dev = Y.device
+    _flat("Y", Y, (rows, N), _BF16_FP32, dev)
+    _need(N >= 8 and N % 8 == 0, f"N={N} must be a multiple of 8")
+    _need(isinstance(position, torch.Tensor) and position.dim() == 2, "position must be a 2-D tensor [T, k]")
+    T, k = position.shape
+    _need(k >= 1, "position must have k >= 1 columns")
+    _flat("position", position, (T, k), _I32, dev, 4)
+    _flat("weights", weights, (T, k), _FP32, dev, 4)
+    dt = Y.dtype
+    if residual is not None:
+        _flat("residual", residual, (T, N), _BF16_FP32, dev)
+        dt = residual.dtype
+    if out is not None:
+        _flat("out", out, (T, N), (dt,) if residual is not None else _BF16_FP32, dev)
+    else:
+        out = torch.empty((T, N), dtype=dt, device=dev)
+    _call("sharq_moe_combine", Y.data_ptr(), 1 if Y.dtype == torch.float32 else 0, rows, N, position.data_ptr(),
+          weights.data_ptr(), T, k, _ptr(residual), out.data_ptr(), 1 if out.dtype == torch.float32 else 0,
+          _stream(dev))
+    return out
+
+
+# ------------------------------------------------- 8-bit integer operands --
+
+@dataclass
+class PreparedInt8:
+    """8-bit tokens with one scale each."""
+    codes: "object"          # int8 [M, K]
+    scales: "object"         # fp32 [M]
+    M: int
+    K: int
+
+    @staticmethod
+    def empty(M: int, K: int, device="cuda") -> "PreparedInt8":
+        return PreparedInt8(torch.empty((M, K), dtype=torch.int8, device=device),
+                            torch.empty((M,), dtype=torch.float32, device=device), M, K)
+
+
+@dataclass
+class WeightInt8:
+    """8-bit weight with one scale for each output channel."""
+    codes: "object"          # int8 [N, K]
+    scales: "object"         # fp32 [N]
+    N: int
+    K: int
+
+    @staticmethod
+    def empty(N: int, K: int, device="cuda") -> "WeightInt8":
+        return WeightInt8(torch.empty((N, K), dtype=torch.int8, device=device),
+                          torch.empty((N,), dtype=torch.float32, device=device), N, K)
+
+
+_I8 = (torch.int8,)
+
+
+def _check_rows8(name: str, q, rows: int, K: int, dev) -> None:
+    _flat(f"{name} codes", q.codes, (rows, K), _I8, dev)
+    _flat(f"{name} scales", q.scales, (rows,), _FP32, dev, 4)
+
+
+def _check_extent(K: int) -> None:
+    _need(8 <= K <= 32768 and K % 8 == 0, f"K={K}, expected a multiple of 8 from 8 to 32768")
+
+
+@_placed
+def prepare_int8(X, gamma=None, eps: float = 1e-6, out: Optional[PreparedInt8] = None) -> PreparedInt8:
+    """X bf16 [M, K] -> 8-bit codes and a scale for each row, after RMSNorm
+    with gamma (bf16 [K]) when it is given."""
+    _need(X.dim() == 2, "X must be a 2-D tensor [M, K]")
+    M, K = X.shape
+    dev = X.device
+    _check_extent(K)
+    _flat("X", X, (M, K), (torch.bfloat16,), dev)
+    if gamma is not None:
+        _flat("gamma", gamma, (K,), (torch.bfloat16,), dev)
+    if out is not None:
+        _need((out.M, out.K) == (M, K), f"out describes M={out.M}, K={out.K}; the call needs M={M}, K={K}")
+        _check_rows8("out", out, M, K, dev)
+    q = out if out is not None else PreparedInt8.empty(M, K, dev)
+    c = _RowsInt8(q.codes.data_ptr(), q.scales.data_ptr(), M, K)
+    _call("sharq_prepare_int8", X.data_ptr(), _ptr(gamma), eps, ctypes.byref(c), _stream(dev))
+    return q
+
+
+@_placed
+def quantize_weight_int8(W, out: Optional[WeightInt8] = None) -> WeightInt8:
+    """W bf16 [N, K] -> 8-bit codes and a scale for each output channel."""
+    _need(W.dim() == 2, "W must be a 2-D tensor [N, K]")
+    N, K = W.shape
+    dev = W.device
+    _need(N >= 1, "W must have at least one row")
+    _check_extent(K)
+    _flat("W", W, (N, K), (torch.bfloat16,), dev)
+    if out is not None:
+        _need((out.N, out.K) == (N, K), f"out describes N={out.N}, K={out.K}; the call needs N={N}, K={K}")
+        _check_rows8("out", out, N, K, dev)
+    w = out if out is not None else WeightInt8.empty(N, K, dev)
+    c = _WeightInt8(w.codes.data_ptr(), w.scales.data_ptr(), N, K)
+    _call("sharq_quantize_weight_int8", W.data_ptr(), ctypes.byref(c), _stream(dev))
+    return w
+
+
+@_placed
+def linear_int8(x: PreparedInt8, w: WeightInt8, bias=None, out_fp32: bool = False, out=None):
+    """Linear in 8-bit integers: Y[i, j] = x.scales[i] * w.scales[j] *
+    sum_k x.codes[i, k] * w.codes[j, k] (+ bias[j]), the sum exact.  bias: bf16
+    or fp32 [N]; Y: bf16, or fp32 with out_fp32."""
+    dev = x.codes.device
+    _need(isinstance(w, WeightInt8), "w must be a WeightInt8")
+    _need(w.K == x.K, f"weight K={w.K} does not match the activations' K={x.K}")
+    _need(16 <= x.K <= 65536 and x.K % 16 == 0, f"K={x.K}, expected a multiple of 16 from 16 to 65536")
+    _need(w.N >= 1, f"N={w.N}, expected at least 1")
+    _check_rows8("x", x, x.M, x.K, dev)
+    _check_rows8("weight", w, w.N, w.K, dev)
+    if bias is not None:
+        _flat("bias", bias, (w.N,), _BF16_FP32, dev, bias.element_size())
+    dt = torch.float32 if out_fp32 else torch.bfloat16
+    if out is not None:
+        _flat("out", out, (x.M, w.N), (dt,), dev)
+    else:
+        out = torch.empty((x.M, w.N), dtype=dt, device=dev)
+    cx = _RowsInt8(x.codes.data_ptr(), x.scales.data_ptr(), x.M, x.K)
+    cw = _WeightInt8(w.codes.data_ptr(), w.scales.data_ptr(), w.N, w.K)
+    _call("sharq_linear_int8", ctypes.byref(cx), ctypes.byref(cw), _ptr(bias),
+          1 if bias is not None and bias.dtype == torch.float32 else 0, out.data_ptr(), 1 if out_fp32 else 0,
+          _stream(dev))
+    return out
+
+
+# ------------------------------------------------------ residual stream --
+
+_NORM = {None: 0, "rms": 1, "layer": 2}
+
+
+@_placed
+def residual_norm(x, h=None, norm: Optional[str] = "rms", post_gamma=None, gate=None, alpha: float = 1.0,
+                  gamma=None, beta=None, scale=None, shift=None, eps: float = 1e-6, int8: bool = False,
+                  out_x=None, out_y=None):
+    """The residual addition with the norms, gate and modulation around it:
+
+        u  = h, or RMSNorm(h) * post_gamma
+        x' = x + alpha * gate * u
+        y  = norm(x') * gamma + beta, then y * (1 + scale) + shift
+
+    norm: "rms", "layer" or None (no y).  x: [M, K] bf16 or fp32, h: [M, K]
+    bf16 or fp32 (rows may be strided); gate, scale, shift: [G, K] (rows may be
+    strided: the chunks of one modulation tensor), row r of M using row
+    r // (M / G).  Returns (x', y): x' in x's type (x itself when h is None),
+    y bf16, or a PreparedInt8 with int8=True, or None.  out_x may be x or h."""
+    _need(x.dim() == 2, "x must be a 2-D tensor [M, K]")
+    M, K = x.shape
+    dev = x.device
+    _check_extent(K)
+    _need(norm in _NORM, f"norm is {norm!r}, expected 'rms', 'layer' or None")
+    a = _ResidualNorm()
+    a.ld_x = _rows("x", x, (M, K), _BF16_FP32, dev)
+    if h is None:
+        _need(post_gamma is None and gate is None, "post_gamma and gate need h")
+        _need(norm is not None, "without h and without a norm there is nothing to compute")
+    else:
+        a.ld_h = _rows("h", h, (M, K), _BF16_FP32, dev)
+    _need(norm is not None or all(v is None for v in (gamma, beta, scale, shift)),
+          "gamma, beta, scale and shift need a norm")
+    _need(norm is not None or not (int8 or out_y is not None), "int8 and out_y need a norm")
+    vec = [(n, v) for n, v in (("post_gamma", post_gamma), ("gamma", gamma), ("beta", beta)) if v is not None]
+    for n, v in vec:
+        _flat(n, v, (K,), _BF16_FP32, dev)
+        _need(v.dtype == vec[0][1].dtype, f"{n} is {v.dtype}, {vec[0][0]} is {vec[0][1].dtype}")
+    mod = [(n, v) for n, v in (("gate", gate), ("scale", scale), ("shift", shift)) if v is not None]
+    G = 1
+    if mod:
+        _need(mod[0][1].dim() == 2, f"{mod[0][0]} must be a 2-D tensor [G, K]")
+        G = mod[0][1].shape[0]
+        _need(G >= 1 and M % G == 0, f"G={G} rows of {mod[0][0]} must divide M={M}")
+        for n, v in mod:
+            ld = _rows(n, v, (G, K), _BF16_FP32, dev)
+            _need(v.dtype == mod[0][1].dtype, f"{n} is {v.dtype}, {mod[0][0]} is {mod[0][1].dtype}")
+            setattr(a, "ld_" + n, ld)
+    if out_x is not None:
+        a.ld_out = _rows("out_x", out_x, (M, K), (x.dtype,), dev)
+        for n, v, ld in (("x", x, a.ld_x), ("h", h, a.ld_h)):
+            _need(v is None or v.data_ptr() != out_x.data_ptr() or (ld == a.ld_out and v.dtype == x.dtype),
+                  f"out_x starts where {n} does but has another layout")
+        a.out_x = out_x.data_ptr()
+    elif h is not None:
+        out_x = torch.empty((M, K), dtype=x.dtype, device=dev)
+        a.out_x, a.ld_out = out_x.data_ptr(), K
+    y, q = None, None
+    if norm is not None:
+        if int8:
+            if out_y is not None:
+                _need(isinstance(out_y, PreparedInt8) and (out_y.M, out_y.K) == (M, K),
+                      f"out_y must be a PreparedInt8 of M={M}, K={K}")
+                _check_rows8("out_y", out_y, M, K, dev)
+            y = out_y if out_y is not None else PreparedInt8.empty(M, K, dev)
+            q = _RowsInt8(y.codes.data_ptr(), y.scales.data_ptr(), M, K)
+            a.q = ctypes.pointer(q)
+        else:
+            if out_y is not None:
+                _flat("out_y", out_y, (M, K), (torch.bfloat16,), dev)
+            y = out_y if out_y is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+            a.y = y.data_ptr()
+    a.x, a.h, a.post_gamma, a.gate = x.data_ptr(), _ptr(h), _ptr(post_gamma), _ptr(gate)
+    a.gamma, a.beta, a.scale, a.shift = _ptr(gamma), _ptr(beta), _ptr(scale), _ptr(shift)
+    a.M, a.G, a.K, a.norm = M, G, K, _NORM[norm]
+    a.x_is_fp32 = x.dtype == torch.float32
+    a.h_is_fp32 = h is not None and h.dtype == torch.float32
+    a.norm_is_fp32 = bool(vec) and vec[0][1].dtype == torch.float32
+    a.mod_is_fp32 = bool(mod) and mod[0][1].dtype == torch.float32
+    a.alpha, a.eps = alpha, eps
+    _call("sharq_residual_norm", ctypes.byref(a), _stream(dev))
+    return out_x if out_x is not None else x, y

@@ -317,6 +317,158 @@ SHARQ_API sharq_status sharq_selftest_prepare_timeout(const void* X_bf16, const 
                                                       void* ws, size_t ws_bytes, int64_t limit_us,
                                                       void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The rest of a layer around its linears: routing to experts, the residual
+ * addition with its norms, and linears in 8-bit integers.  Conventions as
+ * above; extents are freer (stated at each), rows may be further apart than
+ * their length where an `ld` (elements from row to row) is given, and every
+ * row start must be 16-byte aligned unless stated otherwise.  Buffers of one
+ * call must not overlap, except where a call says so.
+ * ------------------------------------------------------------------------ */
+
+/* The experts of each token and the order in which a grouped linear takes
+ * them.  All arrays are device memory, 4-byte aligned. */
+typedef struct {
+    int32_t* ids;        /* [T, k] expert of each choice, -1 for none          */
+    float*   weights;    /* [T, k] its weight, 0 where the id is -1            */
+    int32_t* row_index;  /* [T * k] token of each dispatched row               */
+    int32_t* offsets;    /* [E + 1] first dispatched row of each expert        */
+    int32_t* position;   /* [T, k] dispatched row of each choice, -1 for none  */
+    int64_t  T;
+    int      k, E;
+} sharq_routing;
+
+typedef enum { SHARQ_SCORE_SOFTMAX = 0, SHARQ_SCORE_SIGMOID = 1 } sharq_score;
+typedef enum { SHARQ_GROUP_MAX = 0, SHARQ_GROUP_TOP2 = 1 } sharq_group_score;
+
+typedef struct {
+    int   score;          /* sharq_score: over all E experts, or of each alone   */
+    int   groups;         /* equal groups of neighbouring experts (1: none), <= 32 */
+    int   topk_groups;    /* groups a token may use, 1 .. groups                 */
+    int   group_score;    /* sharq_group_score                                   */
+    int   renormalize;    /* weights of a token sum to 1 (before `scale`)        */
+    float scale;          /* factor of every weight, finite                      */
+} sharq_route_options;
+
+/* Routing: logits [T, E] (fp32, or bf16 with logits_fp32 = 0; row stride ld
+ * elements, no alignment beyond the type's) -> out->ids and out->weights.
+ *   An expert is masked for a token when its logit, or its bias, is -inf or
+ *   NaN; every finite value is a value, the type's lowest included.
+ *   s[e] = softmax over the unmasked experts, or 1 / (1 + exp(-logit));
+ *   c[e] = s[e] + bias[e]  (bias fp32 [E], or NULL for none);
+ *   a group's score is the largest c in it, or the sum of its two largest (a
+ *   missing second counts 0); the topk_groups best groups are kept (lower
+ *   index first on ties; never one whose experts are all masked);
+ *   ids: the k unmasked experts of those groups with the largest c, in
+ *   descending order (lower index first on ties); -1 where there are fewer;
+ *   weights: s (without the bias) of each, divided by their sum when
+ *   renormalize is set (0 when that sum is 0), times scale.
+ * The comparisons decide as they would in 64-bit arithmetic: scores that
+ * fp32 cannot tell apart are evaluated again in double.  A softmax over a
+ * logit of +inf has no value: its weights are NaN.
+ * 1 <= E <= 512, E a multiple of groups, 1 <= k <= 32, k at most the experts
+ * of topk_groups groups, T * k < 2^31.  When out->row_index is not NULL the
+ * dispatch order is built too, as sharq_moe_dispatch. */
+SHARQ_API sharq_status sharq_moe_route(const void* logits, int64_t ld, int logits_fp32,
+                                       const float* bias, const sharq_route_options* opt,
+                                       const sharq_routing* out, void* stream);
+
+/* Dispatch order of r->ids (read; T, k, E filled in): choices sorted by
+ * expert, within an expert by token and then by place in the token's row.
+ * Writes row_index, offsets and position, which sharq_moe_linear and
+ * sharq_moe_combine take.  An id outside 0 .. E-1 is dropped: its position
+ * is -1 and it takes no row, so offsets[E] counts the live rows; row_index
+ * entries from there on are 0, and the grouped linears leave those rows of
+ * their output as they were.  1 <= E <= 512, T * k < 2^31. */
+SHARQ_API sharq_status sharq_moe_dispatch(const sharq_routing* r, void* stream);
+
+/* Expert outputs back to the tokens:
+ *   out[t] = sum_j weights[t, j] * Y[position[t, j]] [+ residual[t]],
+ * summed in fp32 with j ascending and the residual last, rounded once.
+ * Y [rows, N] bf16 or fp32; residual (or NULL) and out [T, N] bf16 or fp32,
+ * alike; out may be the residual itself.  A position outside 0 .. rows-1
+ * adds nothing, whatever its weight.  N % 8 == 0, k >= 1, T <= 2^31 - 1. */
+SHARQ_API sharq_status sharq_moe_combine(const void* Y, int y_is_fp32, int64_t rows, int N,
+                                         const int32_t* position, const float* weights, int64_t T,
+                                         int k, const void* residual, void* out, int out_is_fp32,
+                                         void* stream);
+
+/* 8-bit integer operands: signed codes with one fp32 scale a row. */
+typedef struct {
+    int8_t* codes;       /* [M, K] */
+    float*  scales;      /* [M] */
+    int64_t M;
+    int     K;
+} sharq_prepared_int8;
+
+typedef struct {
+    int8_t* codes;       /* [N, K] */
+    float*  scales;      /* [N] */
+    int     N, K;
+} sharq_weight_int8;
+
+/* The residual stream between two blocks:
+ *   u  = h, or h * rsqrt(mean(h^2) + eps) * post_gamma   (norm after the block)
+ *   x' = x + alpha * gate * u         (x' = x when h is NULL)
+ *   y  = x'                                                SHARQ_NORM_NONE
+ *        x' * rsqrt(mean(x'^2) + eps)                      SHARQ_NORM_RMS
+ *        (x' - mean) * rsqrt(mean((x' - mean)^2) + eps)    SHARQ_NORM_LAYER
+ *   y  = y * gamma + beta, then y * (1 + scale) + shift    (NULL: left out)
+ * in fp32; y is taken from x' before it is rounded to out_x's type.  Outputs
+ * (any may be NULL): out_x in x's type, y as bf16 [M, K], and q, y in 8 bits:
+ *   a = max |y| of the row, scales = a / 127, codes = rne(y * (127 / a)),
+ * the two quotients and the product each rounded to fp32; a row with
+ * a < 2^-100 gets scale 0 and zero codes.  out_x may be x, or h when their
+ * types agree.  gate, scale and shift are [G, K]: row r uses row
+ * r / (M / G); G divides M.  The vectors of a norm (post_gamma, gamma, beta)
+ * share one type, those of the modulation (gate, scale, shift) another,
+ * each bf16 or fp32; norm vectors and modulation need a norm, except gate.
+ * K % 8 == 0, 8 <= K <= 32768, M <= 2^31 - 1.  A row's result does not
+ * depend on M or on other rows. */
+typedef enum { SHARQ_NORM_NONE = 0, SHARQ_NORM_RMS = 1, SHARQ_NORM_LAYER = 2 } sharq_norm;
+
+typedef struct {
+    const void* x;           /* [M, K] bf16, or fp32 with x_is_fp32 */
+    const void* h;           /* [M, K] the block's output, or NULL  */
+    const void* post_gamma;  /* [K] */
+    const void* gate;        /* [G, K] */
+    const void* gamma;       /* [K] */
+    const void* beta;        /* [K] */
+    const void* scale;       /* [G, K] */
+    const void* shift;       /* [G, K] */
+    void*       out_x;
+    void*       y;
+    const sharq_prepared_int8* q;
+    int64_t     ld_x, ld_h, ld_gate, ld_scale, ld_shift, ld_out;
+    int64_t     M, G;
+    int         K, norm;
+    int         x_is_fp32, h_is_fp32, norm_is_fp32, mod_is_fp32;
+    float       alpha, eps;
+} sharq_residual_norm_args;
+
+SHARQ_API sharq_status sharq_residual_norm(const sharq_residual_norm_args* a, void* stream);
+
+/* 8-bit operand of a linear, beside sharq_prepare: X bf16 [M, K], RMSNorm
+ * with gamma bf16 [K] in front (NULL: none), codes and scales as
+ * sharq_residual_norm's q.  Extents as there. */
+SHARQ_API sharq_status sharq_prepare_int8(const void* X_bf16, const void* gamma_bf16, float eps,
+                                          const sharq_prepared_int8* out, void* stream);
+
+/* 8-bit weight, once per layer: W bf16 [N, K] -> codes and a scale for each
+ * output channel, quantised row by row as sharq_prepare_int8. */
+SHARQ_API sharq_status sharq_quantize_weight_int8(const void* W_bf16, const sharq_weight_int8* out,
+                                                  void* stream);
+
+/* Linear in 8-bit integers:
+ *   Y[i, j] = (x.scales[i] * sum_k x[i, k] w[j, k]) * w.scales[j] [+ bias[j]],
+ * the sum exact in 32-bit integers and rounded once to fp32.  bias [N] fp32
+ * (bias_is_fp32) or bf16, or NULL; Y [M, N] bf16 or fp32.  Any codes are
+ * allowed, -128 too.  K % 16 == 0, 16 <= K <= 65536, N >= 1, M >= 0; codes
+ * and Y 16-byte aligned, scales and bias by their type. */
+SHARQ_API sharq_status sharq_linear_int8(const sharq_prepared_int8* x, const sharq_weight_int8* w,
+                                         const void* bias, int bias_is_fp32, void* Y, int y_is_fp32,
+                                         void* stream);
+
 /* Synchronises `stream`, then reads and clears the device status word:
  * SHARQ_OK, SHARQ_ERR_TIMEOUT if a bounded device wait gave up since the
  * last call, or SHARQ_ERR_CUDA if the stream itself reports an error. */
