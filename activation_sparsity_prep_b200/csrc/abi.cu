@@ -4,6 +4,7 @@
 // enqueued; the kernels themselves live in prepare.cu and linear.cu.
 #include "../../include/sharq.h"
 #include "common.cuh"
+#include "ops_internal.h"
 #include "sharq_internal.h"
 
 #include <mutex>
@@ -283,7 +284,7 @@ sharq_status sharq_last_device_status(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return SHARQ_ERR_CUDA;
     unsigned v = sharq::take_status_prepare() | sharq::take_status_linear() |
-                 sharq::take_status_selftest();
+                 sharq::take_status_selftest() | sharq::take_status_int8();
     if (v & sharq::kStatusReadFailed) return SHARQ_ERR_CUDA;
     if (v & (sharq::kStatusGridTimeout | sharq::kStatusMbarTimeout)) return SHARQ_ERR_TIMEOUT;
     if (v) return SHARQ_ERR_CUDA;

@@ -1,8 +1,24 @@
 // int8.cu -- linear in 8-bit integers with a scale for each token and
 // channel (sm_100a):
-//   Y[i, j] = x_scale[i] * w_scale[j] * sum_k x[i, k] w[j, k] [+ bias[j]].
-// The sum is exact in int32 (K <= 65536, so |sum| <= 2^30); it is rounded
-// once to fp32, scaled, biased, and rounded to the output's type.
+//   Y[i, j] = (x_scale[i] * sum_k x[i, k] w[j, k]) * w_scale[j] [+ bias[j]].
+// The sum is exact in int32 (K <= 65536, so |sum| <= 2^30), whatever the
+// order; it is rounded once to fp32, scaled, scaled and biased in one fused
+// step, and rounded to the output's type.  Every form below ends in the same
+// finish(), so a row's result does not depend on the batch around it.
+//
+// Three forms:
+//   dot     few tokens: a warp a channel on the dot-product units, bound by
+//           streaming the weight;
+//   swapped up to 256 tokens: 128 channels x all tokens on the tensor cores
+//           (the weight is the M-side operand), K split over a cluster so
+//           that narrow layers use every SM; bound by the weight;
+//   tiled   128 tokens x up to 256 channels a tile, persistent, bound by the
+//           tensor cores.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+
 #include "common.cuh"
 #include "ops_common.cuh"
 #include "ops_internal.h"
@@ -10,30 +26,36 @@
 namespace sharq {
 namespace {
 
-__device__ __forceinline__ void store_out(const Int8Launch& a, int64_t i, int j, int sum) {
-    float y = (float)sum * a.x_scale[i] * a.w_scale[j];
-    if (a.bias)
-        y += a.bias_fp32 ? static_cast<const float*>(a.bias)[j]
-                         : __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[j]);
+__device__ __forceinline__ float finish(int sum, float xs, float ws, float bias) {
+    return __fmaf_rn(__fmul_rn(__int2float_rn(sum), xs), ws, bias);
+}
+
+__device__ __forceinline__ float bias_at(const Int8Launch& a, int64_t j) {
+    if (!a.bias) return 0.0f;
+    return a.bias_fp32 ? static_cast<const float*>(a.bias)[j]
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[j]);
+}
+
+__device__ __forceinline__ void store_one(const Int8Launch& a, int64_t i, int64_t j, float y) {
     if (a.y_fp32) static_cast<float*>(a.Y)[i * a.N + j] = y;
     else          static_cast<__nv_bfloat16*>(a.Y)[i * a.N + j] = __float2bfloat16_rn(y);
 }
 
-// A warp computes R channels for MT tokens on the dot-product units, its
-// lanes striding K in 16-byte pieces.
+// ---------------------------------------------------------------- dot -----
+// A warp computes R channels for MT tokens, its lanes striding K in 16-byte
+// pieces.
 template <int MT, int R>
 __global__ void __launch_bounds__(256)
 dot_kernel(const Int8Launch a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int j0 = (blockIdx.x * 8 + warp) * R;
-    const int64_t i0 = (int64_t)blockIdx.y * MT;
     if (j0 >= a.N) return;
     const int4* w[R];
     const int4* x[MT];
 #pragma unroll
     for (int r = 0; r < R; ++r) w[r] = reinterpret_cast<const int4*>(a.w + (int64_t)min(j0 + r, a.N - 1) * a.K);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) x[m] = reinterpret_cast<const int4*>(a.x + min(i0 + m, a.M - 1) * a.K);
+    for (int m = 0; m < MT; ++m) x[m] = reinterpret_cast<const int4*>(a.x + min((int64_t)m, a.M - 1) * a.K);
     int acc[MT][R] = {};
     for (int c = lane; c < a.K / 16; c += 32) {
         int4 wv[R];
@@ -52,33 +74,467 @@ dot_kernel(const Int8Launch a) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int sum = __reduce_add_sync(kFull, acc[m][r]);
-            if (lane == 0 && i0 + m < a.M && j0 + r < a.N) store_out(a, i0 + m, j0 + r, sum);
+            if (lane == 0 && m < a.M && j0 + r < a.N)
+                store_one(a, m, j0 + r, finish(sum, a.x_scale[m], a.w_scale[j0 + r], bias_at(a, j0 + r)));
         }
 }
 
 template <int MT>
 cudaError_t launch_dot(const Int8Launch& p, cudaStream_t s) {
     constexpr int R = 4;
-    dim3 grid((unsigned)((p.N + 8 * R - 1) / (8 * R)), 1);
-    // grid.y holds at most 65535 token tiles: longer batches go in parts
-    Int8Launch q = p;
-    for (int64_t i = 0; i < p.M; i += (int64_t)MT * 65535) {
-        q.M = p.M - i < (int64_t)MT * 65535 ? p.M - i : (int64_t)MT * 65535;
-        q.x = p.x + i * p.K;
-        q.x_scale = p.x_scale + i;
-        q.Y = static_cast<char*>(p.Y) + i * p.N * (p.y_fp32 ? 4 : 2);
-        grid.y = (unsigned)((q.M + MT - 1) / MT);
-        dot_kernel<MT, R><<<grid, 256, 0, s>>>(q);
-        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    dot_kernel<MT, R><<<(unsigned)((p.N + 8 * R - 1) / (8 * R)), 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------- tensor cores -----
+constexpr int kRows = 128;                    // rows of the M-side operand of a tile
+constexpr int kStep = 128;                    // K a pipeline stage: one 128-byte swizzled row
+constexpr uint32_t kABytes = kRows * kStep;
+constexpr int kMaxStages = 8;
+constexpr int kI8Threads = 192;               // TMA warp, MMA warp, four epilogue warps
+
+struct alignas(8) I8Barriers {
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint32_t tmem_base;
+};
+
+// D (s32, tensor memory) (+)= A (s8, shared) x B (s8, shared)^T, 32 of K.
+__device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// Instruction descriptor: s32 accumulator (2 at bit 4), signed 8-bit A and B
+// (1 at bits 7 and 10), N >> 3 at bit 17, M >> 4 at bit 24.
+__host__ __device__ constexpr uint32_t i8_idesc(int n) {
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+
+struct Geometry {
+    int bn;                  // rows of the N-side operand of a tile
+    int stages;
+    int mt, nt;              // tiles along the M-side and the N-side operand
+    int n_fast;              // tile walk: N-side fastest
+    int split;               // swapped form: blocks of a cluster that share a tile's K
+    uint32_t tmem_cols;
+};
+
+__device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ int ld_shared_cluster_s32(const int* p, uint32_t rank) {
+    return __float_as_int(ld_shared_cluster_f32(p, rank));
+}
+
+// Issues the TMA loads of k-steps [k0, k1) of one tile.
+__device__ __forceinline__ bool produce(const CUtensorMap* ta, const CUtensorMap* tb, I8Barriers* bars, uint8_t* smem,
+                                        uint32_t stride, int stages, uint32_t& it, int k0, int k1, int arow, int brow) {
+    for (int k = k0; k < k1; ++k, ++it) {
+        const uint32_t s = it % stages;
+        if (it >= (uint32_t)stages && !mbar_wait(&bars->empty[s], ((it / stages) - 1) & 1)) return false;
+        uint8_t* st = smem + s * stride;
+        mbar_arrive_expect_tx(&bars->full[s], stride);
+        tma_load_2d(st, ta, &bars->full[s], k * kStep, arow);
+        tma_load_2d(st + kABytes, tb, &bars->full[s], k * kStep, brow);
     }
-    return cudaSuccess;
+    return true;
+}
+
+// Waits (bounded) for the loads still in flight after an early end.
+__device__ __forceinline__ void drain(I8Barriers* bars, int stages, uint32_t it) {
+    for (uint32_t i = it > (uint32_t)stages ? it - stages : 0; i < it; ++i) mbar_wait(&bars->full[i % stages], (i / stages) & 1);
+}
+
+// Multiplies nk staged k-steps into the accumulator at tensor-memory address d.
+__device__ __forceinline__ bool multiply(I8Barriers* bars, uint8_t* smem, uint32_t stride, int stages, uint32_t& it,
+                                         int nk, uint32_t d, uint32_t idesc) {
+    for (int k = 0; k < nk; ++k, ++it) {
+        const uint32_t s = it % stages;
+        if (!mbar_wait(&bars->full[s], (it / stages) & 1)) return false;
+        tc_fence_after();
+        const uint32_t at = smem_u32(smem + s * stride);
+#pragma unroll
+        for (int j = 0; j < kStep / 32; ++j)
+            tc_mma_i8(d, sdesc_sw128(at + 32 * j), sdesc_sw128(at + kABytes + 32 * j), idesc, (k | j) ? 1u : 0u);
+        tc_commit(&bars->empty[s]);
+    }
+    return true;
+}
+
+__device__ __forceinline__ uint8_t* setup(uint8_t* raw, const Geometry& g, uint32_t stride, I8Barriers*& bars,
+                                          uint8_t*& tail) {
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    tail = smem + g.stages * stride;
+    bars = reinterpret_cast<I8Barriers*>(tail);
+    tail += (sizeof(I8Barriers) + 127) / 128 * 128;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < g.stages; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars->acc_full[b], 1);
+            mbar_init(&bars->acc_empty[b], 4);
+        }
+        fence_barrier_init();
+    }
+    if (threadIdx.x >> 5 == 1) { tmem_alloc(&bars->tmem_base, g.tmem_cols); tmem_relinquish(); }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return smem;
+}
+
+__device__ __forceinline__ void tile_at(const Geometry& g, int t, int& m, int& n) {
+    if (g.n_fast) { m = t / g.nt; n = t - m * g.nt; }
+    else          { n = t / g.mt; m = t - n * g.mt; }
+}
+
+// Tiled form.  A = tokens, B = channels; two accumulators of bn columns, so
+// the next tile's MMAs run while the epilogue drains the previous one.  A
+// thread drains one token's columns, 128 bytes of output at a time, through
+// a staging buffer that turns them into whole 128-byte row segments.
+template <bool YF32>
+__global__ void __launch_bounds__(kI8Threads, 1)
+tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const Int8Launch a,
+             const Geometry g) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t stride = kABytes + g.bn * kStep;
+    I8Barriers* bars;
+    uint8_t* tail;
+    uint8_t* smem = setup(smem_raw, g, stride, bars, tail);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tmem = bars->tmem_base;
+    const int nk = (a.K + kStep - 1) / kStep;
+    const int tiles = g.mt * g.nt;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_tmap(&ta); prefetch_tmap(&tb);
+            uint32_t it = 0;
+            for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+                int m, n;
+                tile_at(g, t, m, n);
+                if (!produce(&ta, &tb, bars, smem, stride, g.stages, it, 0, nk, m * kRows, n * g.bn)) {
+                    drain(bars, g.stages, it);
+                    break;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0, tc = 0;
+            for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++tc) {
+                const uint32_t buf = tc & 1, use = tc >> 1;
+                if (use > 0 && !mbar_wait(&bars->acc_empty[buf], (use - 1) & 1)) break;
+                tc_fence_after();
+                if (!multiply(bars, smem, stride, g.stages, it, nk, tmem + buf * g.bn, i8_idesc(g.bn))) break;
+                tc_commit(&bars->acc_full[buf]);
+            }
+        }
+    } else {
+        constexpr int kCols = YF32 ? 32 : 64;             // columns of one staged 128-byte row segment
+        const int q = warp & 3;
+        const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+        uint8_t* stage = tail + q * 4096;                 // [32 rows][128 bytes], 16-byte units swizzled by row
+        float* col_scale = reinterpret_cast<float*>(tail + 4 * 4096);
+        float* col_bias = col_scale + 256;
+        const int et = threadIdx.x - 64;
+        const bool vec = (int64_t)a.N % (YF32 ? 4 : 8) == 0;
+        uint32_t tc = 0;
+        bool ok = true;                                   // after a wait that gave up: keep step, store nothing
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++tc) {
+            int m, n;
+            tile_at(g, t, m, n);
+            const int64_t row0 = (int64_t)m * kRows + q * 32, col0 = (int64_t)n * g.bn;
+            epilogue_bar();                               // the previous tile's columns are no longer read
+            for (int c = et; c < g.bn; c += 128) {
+                const bool in = col0 + c < a.N;
+                col_scale[c] = in ? a.w_scale[col0 + c] : 0.0f;
+                col_bias[c] = in ? bias_at(a, col0 + c) : 0.0f;
+            }
+            epilogue_bar();
+            const float xs = row0 + lane < a.M ? a.x_scale[row0 + lane] : 0.0f;
+            const uint32_t buf = tc & 1, use = tc >> 1;
+            ok = __all_sync(kFull, ok && mbar_wait(&bars->acc_full[buf], use & 1));
+            tc_fence_after();
+            if (!ok) continue;
+            for (int c0 = 0; c0 < g.bn; c0 += kCols) {
+                uint32_t v[kCols];
+#pragma unroll
+                for (int h = 0; h < kCols; h += 32)
+                    tmem_ld_32x32b_x32(tmem + buf * g.bn + lane_off + c0 + h, *reinterpret_cast<uint32_t(*)[32]>(v + h));
+                tmem_ld_wait();
+                if (c0 + kCols >= g.bn) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->acc_empty[buf]);
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {             // 16-byte units of the row segment
+                    uint4 o;
+                    uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (YF32) {
+                            const int c = u * 4 + i;
+                            w[i] = __float_as_uint(finish((int)v[c], xs, col_scale[c0 + c], col_bias[c0 + c]));
+                        } else {
+                            const int c = u * 8 + i * 2;
+                            w[i] = pack_bf16(finish((int)v[c], xs, col_scale[c0 + c], col_bias[c0 + c]),
+                                             finish((int)v[c + 1], xs, col_scale[c0 + c + 1], col_bias[c0 + c + 1]));
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = o;
+                }
+                __syncwarp();
+                if (vec) {
+                    constexpr int kPer = YF32 ? 4 : 8;    // elements of a unit
+                    const int u = lane & 7;
+                    const int64_t col = col0 + c0 + u * kPer;
+#pragma unroll
+                    for (int r8 = 0; r8 < 8; ++r8) {
+                        const int r = r8 * 4 + (lane >> 3);
+                        const uint4 o = *reinterpret_cast<const uint4*>(stage + r * 128 + ((u ^ (r & 7)) << 4));
+                        if (row0 + r < a.M && col < a.N)
+                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.Y) +
+                                                      ((row0 + r) * a.N + col) * (YF32 ? 4 : 2)) = o;
+                    }
+                } else {
+                    for (int r = 0; r < 32 && row0 + r < a.M; ++r)
+                        for (int c = lane; c < kCols; c += 32) {
+                            if (col0 + c0 + c >= a.N) continue;
+                            const int byte = c * (YF32 ? 4 : 2);
+                            const uint8_t* from = stage + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
+                            if constexpr (YF32)
+                                static_cast<float*>(a.Y)[(row0 + r) * a.N + col0 + c0 + c] = *reinterpret_cast<const float*>(from);
+                            else
+                                static_cast<uint16_t*>(a.Y)[(row0 + r) * a.N + col0 + c0 + c] = *reinterpret_cast<const uint16_t*>(from);
+                        }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) { tc_fence_after(); tmem_dealloc(tmem, g.tmem_cols); }
+}
+
+// Swapped form.  A = 128 channels, B = all M <= bn tokens; the `split` blocks
+// of a cluster take a run of k-steps each, leave their int32 partial tiles in
+// shared memory, and every block then adds up and finishes its share of the
+// tokens over distributed shared memory (integer sums: exact in any order).
+__global__ void __launch_bounds__(kI8Threads)
+swapped_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const Int8Launch a,
+               const Geometry g) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t stride = kABytes + g.bn * kStep;
+    I8Barriers* bars;
+    uint8_t* tail;
+    uint8_t* smem = setup(smem_raw, g, stride, bars, tail);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tmem = bars->tmem_base;
+    const int nk = (a.K + kStep - 1) / kStep;
+    const int tile = blockIdx.x / g.split, rank = blockIdx.x - tile * g.split;
+    const int k0 = (int)((int64_t)nk * rank / g.split), k1 = (int)((int64_t)nk * (rank + 1) / g.split);
+    int* partial = reinterpret_cast<int*>(smem);          // [tokens][128], over the stages once they are consumed
+
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_tmap(&tw); prefetch_tmap(&tx);
+            uint32_t it = 0;
+            if (!produce(&tw, &tx, bars, smem, stride, g.stages, it, k0, k1, tile * kRows, 0)) drain(bars, g.stages, it);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            if (multiply(bars, smem, stride, g.stages, it, k1 - k0, tmem, i8_idesc(g.bn))) tc_commit(&bars->acc_full[0]);
+        }
+    }
+    __syncwarp();
+    const int q = warp & 3;
+    const int jl = q * 32 + lane;
+    const int64_t j = (int64_t)tile * kRows + jl;
+    float ws = 0.0f, bias = 0.0f;
+    const int M = (int)a.M;
+    if (warp >= 2) {
+        if (j < a.N) { ws = a.w_scale[j]; bias = bias_at(a, j); }
+        const bool ok = mbar_wait(&bars->acc_full[0], 0);
+        tc_fence_after();
+        if (__all_sync(kFull, ok)) {
+            for (int c0 = 0; c0 < M; c0 += 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (c0 + i >= M) break;
+                    if (g.split > 1) partial[(c0 + i) * kRows + jl] = (int)v[i];
+                    else if (j < a.N) store_one(a, c0 + i, j, finish((int)v[i], a.x_scale[c0 + i], ws, bias));
+                }
+            }
+        }
+    }
+    __syncwarp();
+    if (g.split > 1) {
+        cluster_sync_all();
+        if (warp >= 2 && j < a.N) {
+            const int t0 = M * rank / g.split, t1 = M * (rank + 1) / g.split;
+            for (int i = t0; i < t1; ++i) {
+                int sum = 0;
+                for (int r = 0; r < g.split; ++r) sum += ld_shared_cluster_s32(&partial[i * kRows + jl], r);
+                store_one(a, i, j, finish(sum, a.x_scale[i], ws, bias));
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();                               // no block leaves while its partial tile is read
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) { tc_fence_after(); tmem_dealloc(tmem, g.tmem_cols); }
+}
+
+// ------------------------------------------------------------------ host --
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_tiled() {
+    static const EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeFn>(p);
+        return static_cast<EncodeFn>(nullptr);
+    }();
+    return fn;
+}
+
+// [rows, K] bytes in boxes of box_rows x 128, 128-byte swizzle; what lies
+// past the rows or past K reads as zero.
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int K, int box_rows) {
+    EncodeFn fn = encode_tiled();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)K};
+    cuuint32_t box[2] = {(cuuint32_t)kStep, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class Fn>
+cudaError_t smem_limit_once(std::atomic<bool> (&done)[64], Fn kernel) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+constexpr uint32_t kBarBytes = (sizeof(I8Barriers) + 127) / 128 * 128;
+constexpr uint32_t kEpilogueBytes = 4 * 4096 + 2 * 256 * 4;
+
+uint32_t tmem_cols(int n) {
+    uint32_t c = 32;
+    while (c < (uint32_t)n) c *= 2;
+    return c;
+}
+
+template <bool YF32>
+cudaError_t launch_tiled_t(const CUtensorMap& ta, const CUtensorMap& tb, const Int8Launch& p, const Geometry& g,
+                           size_t smem, int grid, cudaStream_t s) {
+    static std::atomic<bool> done[64];
+    if (cudaError_t e = smem_limit_once(done, tiled_kernel<YF32>); e != cudaSuccess) return e;
+    tiled_kernel<YF32><<<grid, kI8Threads, smem, s>>>(ta, tb, p, g);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_tiled(const Int8Launch& p, cudaStream_t s, int sms) {
+    Geometry g{};
+    g.mt = (int)((p.M + kRows - 1) / kRows);
+    // tile width: the one whose waves over the SMs take least MMA time; a
+    // narrow tile re-reads the tokens more often and is charged for 32 more
+    // columns than it has
+    int64_t best = 0;
+    for (int bn = 256; bn >= 64; bn -= 64) {
+        const int64_t tiles = (int64_t)g.mt * ((p.N + bn - 1) / bn);
+        const int64_t cost = (tiles + sms - 1) / sms * (bn + 32);
+        if (!best || cost < best) { best = cost; g.bn = bn; }
+    }
+    g.nt = (p.N + g.bn - 1) / g.bn;
+    g.n_fast = p.M > p.N;                                 // the smaller operand stays in L2
+    g.split = 1;
+    g.tmem_cols = tmem_cols(2 * g.bn);
+    const uint32_t stride = kABytes + g.bn * kStep;
+    g.stages = std::min<int>(kMaxStages, (int)((227 * 1024 - 1024 - kBarBytes - kEpilogueBytes) / stride));
+    const size_t smem = 1024 + g.stages * stride + kBarBytes + kEpilogueBytes;
+    CUtensorMap ta, tb;
+    if (!make_map(&ta, p.x, p.M, p.K, kRows) || !make_map(&tb, p.w, p.N, p.K, g.bn)) return cudaErrorInvalidValue;
+    const int64_t tiles = (int64_t)g.mt * g.nt;
+    if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+    const int grid = (int)std::min<int64_t>(tiles, std::max(1, sms));
+    return p.y_fp32 ? launch_tiled_t<true>(ta, tb, p, g, smem, grid, s) : launch_tiled_t<false>(ta, tb, p, g, smem, grid, s);
+}
+
+cudaError_t launch_swapped(const Int8Launch& p, cudaStream_t s, int sms) {
+    Geometry g{};
+    g.bn = (int)((p.M + 15) / 16 * 16);
+    g.mt = (p.N + kRows - 1) / kRows;
+    g.nt = 1;
+    g.tmem_cols = tmem_cols(g.bn);
+    const int nk = (p.K + kStep - 1) / kStep;
+    // fewer tiles than SMs: split K so that a cluster of blocks shares a
+    // tile, each keeping at least 4 k-steps
+    g.split = std::max(1, std::min({8, nk / 4, std::max(1, sms) / g.mt}));
+    const uint32_t stride = kABytes + g.bn * kStep;
+    // two blocks an SM where their stages fit: one loads while the other finishes
+    const uint32_t room = (g.bn <= 64 ? 112 : 226) * 1024 - 1024 - kBarBytes;
+    g.stages = std::min<int>({kMaxStages, (int)(room / stride), std::max(2, (nk + g.split - 1) / g.split)});
+    uint32_t need = g.stages * stride;
+    if (g.split > 1) need = std::max<uint32_t>(need, (uint32_t)p.M * kRows * 4);
+    // the partial tiles lie over the stages: keep the barriers behind both
+    while (g.stages * stride < need) ++g.stages;
+    const size_t smem = 1024 + g.stages * stride + kBarBytes;
+    CUtensorMap tw, tx;
+    if (!make_map(&tw, p.w, p.N, p.K, kRows) || !make_map(&tx, p.x, p.M, p.K, g.bn)) return cudaErrorInvalidValue;
+    static std::atomic<bool> done[64];
+    if (cudaError_t e = smem_limit_once(done, swapped_kernel); e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(g.mt * g.split));
+    cfg.blockDim = dim3(kI8Threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = g.split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g.split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, swapped_kernel, tw, tx, p, g);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_int8(const Int8Launch& p, cudaStream_t s, int) {
+unsigned take_status_int8() { return take_tu_status(); }
+
+cudaError_t launch_linear_int8(const Int8Launch& p, cudaStream_t s, int sms) {
     if (p.M == 0) return cudaSuccess;
-    return p.M == 1 ? launch_dot<1>(p, s) : p.M <= 4 ? launch_dot<4>(p, s) : launch_dot<8>(p, s);
+    if (p.M == 1) return launch_dot<1>(p, s);
+    if (p.M <= 4) return launch_dot<4>(p, s);
+    if (p.M <= 8) return launch_dot<8>(p, s);
+    if (p.M <= 256) return launch_swapped(p, s, sms);
+    return launch_tiled(p, s, sms);
 }
 
 }  // namespace sharq

@@ -77,4 +77,7 @@ struct Int8Launch {
 };
 cudaError_t launch_linear_int8(const Int8Launch& p, cudaStream_t s, int sms);
 
+// Reads and clears int8.cu's device status word.
+unsigned take_status_int8();
+
 }  // namespace sharq
