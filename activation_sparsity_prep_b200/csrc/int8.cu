@@ -124,43 +124,79 @@ struct Geometry {
     uint32_t tmem_cols;
 };
 
+// Bounded wait.  mbar_wait() reads the global timer as soon as a first try
+// fails, and that read takes longer than a k-step; a try suspends the thread
+// by itself, so a few hundred of them come first.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity);
+}
+
 __device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __device__ __forceinline__ int ld_shared_cluster_s32(const int* p, uint32_t rank) {
     return __float_as_int(ld_shared_cluster_f32(p, rank));
 }
 
+// One lane of a converged warp.  The TMA and MMA warps run their loops with
+// all lanes and elect one around the instructions: loop state and descriptors
+// then stay in uniform registers, and an issued MMA costs a few cycles
+// instead of the 66 of a loop that only lane 0 runs.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Place in the ring of stages: the stage's index and the parity of its phase.
+struct Ring {
+    uint32_t s, phase;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == (uint32_t)stages) { s = 0; phase ^= 1; }
+    }
+};
+
 // Issues the TMA loads of k-steps [k0, k1) of one tile.
 __device__ __forceinline__ bool produce(const CUtensorMap* ta, const CUtensorMap* tb, I8Barriers* bars, uint8_t* smem,
-                                        uint32_t stride, int stages, uint32_t& it, int k0, int k1, int arow, int brow) {
-    for (int k = k0; k < k1; ++k, ++it) {
-        const uint32_t s = it % stages;
-        if (it >= (uint32_t)stages && !mbar_wait(&bars->empty[s], ((it / stages) - 1) & 1)) return false;
-        uint8_t* st = smem + s * stride;
-        mbar_arrive_expect_tx(&bars->full[s], stride);
-        tma_load_2d(st, ta, &bars->full[s], k * kStep, arow);
-        tma_load_2d(st + kABytes, tb, &bars->full[s], k * kStep, brow);
+                                        uint32_t stride, int stages, Ring& at, int k0, int k1, int arow, int brow) {
+    for (int k = k0; k < k1; ++k, at.next(stages)) {
+        if (!__all_sync(kFull, wait_bar(&bars->empty[at.s], at.phase ^ 1))) return false;
+        uint8_t* st = smem + at.s * stride;
+        if (elect_one()) {
+            mbar_arrive_expect_tx(&bars->full[at.s], stride);
+            tma_load_2d(st, ta, &bars->full[at.s], k * kStep, arow);
+            tma_load_2d(st + kABytes, tb, &bars->full[at.s], k * kStep, brow);
+        }
+        __syncwarp();
     }
     return true;
 }
 
-// Waits (bounded) for the loads still in flight after an early end.
-__device__ __forceinline__ void drain(I8Barriers* bars, int stages, uint32_t it) {
-    for (uint32_t i = it > (uint32_t)stages ? it - stages : 0; i < it; ++i) mbar_wait(&bars->full[i % stages], (i / stages) & 1);
+// Waits (bounded) for the loads still in flight after an early end: those of
+// the stages behind the last one issued whose phase has not completed.
+__device__ __forceinline__ void drain(I8Barriers* bars, int stages, Ring at, bool wrapped) {
+    for (int i = 0; i < stages; ++i) {
+        const uint32_t parity = i < (int)at.s ? at.phase : at.phase ^ 1;
+        if (i < (int)at.s || wrapped) wait_bar(&bars->full[i], parity);
+    }
 }
 
 // Multiplies nk staged k-steps into the accumulator at tensor-memory address d.
-__device__ __forceinline__ bool multiply(I8Barriers* bars, uint8_t* smem, uint32_t stride, int stages, uint32_t& it,
+__device__ __forceinline__ bool multiply(I8Barriers* bars, uint64_t desc0, uint32_t stride, int stages, Ring& at,
                                          int nk, uint32_t d, uint32_t idesc) {
-    for (int k = 0; k < nk; ++k, ++it) {
-        const uint32_t s = it % stages;
-        if (!mbar_wait(&bars->full[s], (it / stages) & 1)) return false;
+    for (int k = 0; k < nk; ++k, at.next(stages)) {
+        if (!__all_sync(kFull, wait_bar(&bars->full[at.s], at.phase))) return false;
         tc_fence_after();
-        const uint32_t at = smem_u32(smem + s * stride);
+        const uint64_t da = desc0 + at.s * (stride >> 4), db = da + (kABytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < kStep / 32; ++j)
-            tc_mma_i8(d, sdesc_sw128(at + 32 * j), sdesc_sw128(at + kABytes + 32 * j), idesc, (k | j) ? 1u : 0u);
-        tc_commit(&bars->empty[s]);
+            for (int j = 0; j < kStep / 32; ++j)
+                tc_mma_i8(d, da + 2 * j, db + 2 * j, idesc, (k | j) ? 1u : 0u);
+            tc_commit(&bars->empty[at.s]);
+        }
+        __syncwarp();
     }
     return true;
 }
@@ -207,34 +243,35 @@ tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUt
     I8Barriers* bars;
     uint8_t* tail;
     uint8_t* smem = setup(smem_raw, g, stride, bars, tail);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t tmem = bars->tmem_base;
+    const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t tmem = __shfl_sync(kFull, bars->tmem_base, 0);
     const int nk = (a.K + kStep - 1) / kStep;
     const int tiles = g.mt * g.nt;
 
     if (warp == 0) {
-        if (lane == 0) {
-            prefetch_tmap(&ta); prefetch_tmap(&tb);
-            uint32_t it = 0;
-            for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-                int m, n;
-                tile_at(g, t, m, n);
-                if (!produce(&ta, &tb, bars, smem, stride, g.stages, it, 0, nk, m * kRows, n * g.bn)) {
-                    drain(bars, g.stages, it);
-                    break;
-                }
+        if (elect_one()) { prefetch_tmap(&ta); prefetch_tmap(&tb); }
+        __syncwarp();
+        Ring at{0, 0};
+        int done = 0;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x, done = 1) {
+            int m, n;
+            tile_at(g, t, m, n);
+            if (!produce(&ta, &tb, bars, smem, stride, g.stages, at, 0, nk, m * kRows, n * g.bn)) {
+                drain(bars, g.stages, at, done || at.phase);
+                break;
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0, tc = 0;
-            for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++tc) {
-                const uint32_t buf = tc & 1, use = tc >> 1;
-                if (use > 0 && !mbar_wait(&bars->acc_empty[buf], (use - 1) & 1)) break;
-                tc_fence_after();
-                if (!multiply(bars, smem, stride, g.stages, it, nk, tmem + buf * g.bn, i8_idesc(g.bn))) break;
-                tc_commit(&bars->acc_full[buf]);
-            }
+        Ring at{0, 0};
+        const uint64_t desc0 = sdesc_sw128(smem_u32(smem));
+        uint32_t tc = 0;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++tc) {
+            const uint32_t buf = tc & 1, use = tc >> 1;
+            if (use > 0 && !__all_sync(kFull, wait_bar(&bars->acc_empty[buf], (use - 1) & 1))) break;
+            tc_fence_after();
+            if (!multiply(bars, desc0, stride, g.stages, at, nk, tmem + buf * g.bn, i8_idesc(g.bn))) break;
+            if (elect_one()) tc_commit(&bars->acc_full[buf]);
+            __syncwarp();
         }
     } else {
         constexpr int kCols = YF32 ? 32 : 64;             // columns of one staged 128-byte row segment
@@ -260,7 +297,7 @@ tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUt
             epilogue_bar();
             const float xs = row0 + lane < a.M ? a.x_scale[row0 + lane] : 0.0f;
             const uint32_t buf = tc & 1, use = tc >> 1;
-            ok = __all_sync(kFull, ok && mbar_wait(&bars->acc_full[buf], use & 1));
+            ok = __all_sync(kFull, ok && wait_bar(&bars->acc_full[buf], use & 1));
             tc_fence_after();
             if (!ok) continue;
             for (int c0 = 0; c0 < g.bn; c0 += kCols) {
@@ -337,24 +374,23 @@ swapped_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     I8Barriers* bars;
     uint8_t* tail;
     uint8_t* smem = setup(smem_raw, g, stride, bars, tail);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t tmem = bars->tmem_base;
+    const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t tmem = __shfl_sync(kFull, bars->tmem_base, 0);
     const int nk = (a.K + kStep - 1) / kStep;
     const int tile = blockIdx.x / g.split, rank = blockIdx.x - tile * g.split;
     const int k0 = (int)((int64_t)nk * rank / g.split), k1 = (int)((int64_t)nk * (rank + 1) / g.split);
     int* partial = reinterpret_cast<int*>(smem);          // [tokens][128], over the stages once they are consumed
 
     if (warp == 0) {
-        if (lane == 0) {
-            prefetch_tmap(&tw); prefetch_tmap(&tx);
-            uint32_t it = 0;
-            if (!produce(&tw, &tx, bars, smem, stride, g.stages, it, k0, k1, tile * kRows, 0)) drain(bars, g.stages, it);
-        }
+        if (elect_one()) { prefetch_tmap(&tw); prefetch_tmap(&tx); }
+        __syncwarp();
+        Ring at{0, 0};
+        if (!produce(&tw, &tx, bars, smem, stride, g.stages, at, k0, k1, tile * kRows, 0))
+            drain(bars, g.stages, at, at.phase);
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            if (multiply(bars, smem, stride, g.stages, it, k1 - k0, tmem, i8_idesc(g.bn))) tc_commit(&bars->acc_full[0]);
-        }
+        Ring at{0, 0};
+        if (multiply(bars, sdesc_sw128(smem_u32(smem)), stride, g.stages, at, k1 - k0, tmem, i8_idesc(g.bn)) && elect_one())
+            tc_commit(&bars->acc_full[0]);
     }
     __syncwarp();
     const int q = warp & 3;
@@ -364,7 +400,7 @@ swapped_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     const int M = (int)a.M;
     if (warp >= 2) {
         if (j < a.N) { ws = a.w_scale[j]; bias = bias_at(a, j); }
-        const bool ok = mbar_wait(&bars->acc_full[0], 0);
+        const bool ok = wait_bar(&bars->acc_full[0], 0);
         tc_fence_after();
         if (__all_sync(kFull, ok)) {
             for (int c0 = 0; c0 < M; c0 += 16) {
