@@ -79,22 +79,18 @@ def _stream(dev) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
-def _need(cond: bool, msg: str) -> None:
-    if not cond:
-        raise ValueError(msg)
-
-
 def _placed(fn):
     """Run a call on its first tensor's device and, when given, on `stream`:
     kernels, allocations and frees then all belong to that stream."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
         t = first.codes if isinstance(first, (PreparedInt8, WeightInt8)) else first
-        _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{fn.__name__} needs CUDA tensors")
-        if stream is None and t.device.index == torch.cuda.current_device():
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{fn.__name__} needs CUDA tensors")
+        if stream is None and t.device.index == torch._C._cuda_getDevice():
             return fn(first, *args, **kw)
-        _need(stream is None or stream.device == t.device, f"the stream is on {stream and stream.device}, "
-              f"the tensors on {t.device}")
+        if stream is not None and stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
         with torch.cuda.device(t.device), torch.cuda.stream(stream):
             return fn(first, *args, **kw)
     return call
@@ -105,26 +101,37 @@ _BF16_FP32 = (torch.bfloat16, torch.float32)
 
 def _flat(name: str, t, shape: Tuple[int, ...], dtypes, dev, align: int = 16):
     """t: a contiguous tensor of `shape` and one of `dtypes` on `dev`."""
-    _need(isinstance(t, torch.Tensor), f"{name} is required")
-    _need(tuple(t.shape) == shape, f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    _need(t.dtype in dtypes, f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    _need(t.device == dev, f"{name} is on {t.device}, expected {dev}")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
-    _need(t.data_ptr() % align == 0, f"{name} must start on a {align}-byte boundary")
+    _kind(name, t, shape, dtypes, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.data_ptr() % align:
+        raise ValueError(f"{name} must start on a {align}-byte boundary")
+
+
+def _kind(name: str, t, shape, dtypes, dev):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is required")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
 def _rows(name: str, t, shape: Tuple[int, int], dtypes, dev, align: int = 16) -> int:
     """t: [rows, K] with unit stride along K, any row stride of whole
     `align` bytes; returns that stride in elements."""
-    _need(isinstance(t, torch.Tensor), f"{name} is required")
-    _need(tuple(t.shape) == shape, f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    _need(t.dtype in dtypes, f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    _need(t.device == dev, f"{name} is on {t.device}, expected {dev}")
-    _need(shape[1] == 1 or t.stride(1) == 1, f"{name} must have unit stride along its rows")
-    ld = t.stride(0) if shape[0] > 1 else shape[1]
-    _need(ld >= shape[1], f"{name} must not overlap itself (row stride {ld})")
-    _need(t.data_ptr() % align == 0 and (ld * t.element_size()) % align == 0,
-          f"every row of {name} must start on a {align}-byte boundary")
+    _kind(name, t, shape, dtypes, dev)
+    ld, unit = t.stride()
+    if unit != 1 and shape[1] != 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    if shape[0] <= 1:
+        ld = shape[1]
+    elif ld < shape[1]:
+        raise ValueError(f"{name} must not overlap itself (row stride {ld})")
+    if t.data_ptr() % align or (shape[0] > 1 and ld * t.element_size() % align):
+        raise ValueError(f"every row of {name} must start on a {align}-byte boundary")
     return ld
 
 
@@ -151,14 +158,14 @@ class Routing:
 
     @staticmethod
     def empty(T: int, k: int, E: int, device="cuda") -> "Routing":
+        # one allocation; every part starts on a 16-byte boundary
         n = T * k
-        # one allocation; the parts start on 16-byte boundaries
-        at = [0]
-        for size in (n, n, n, E + 1, n):
-            at.append(at[-1] + (size + 3) // 4 * 4)
-        b = torch.empty((at[-1],), dtype=torch.int32, device=device)
-        part = [b[o:o + s] for o, s in zip(at, (n, n, n, E + 1, n))]
-        return Routing(part[0].view(T, k), part[1].view(torch.float32).view(T, k), part[2], part[3], part[4].view(T, k))
+        pad, off = (n + 3) // 4 * 4, (E + 4) // 4 * 4
+        b = torch.empty((4 * pad + off,), dtype=torch.int32, device=device)
+        grid, rows = (T, k), (k, 1)
+        return Routing(b.as_strided(grid, rows, 0), b.view(torch.float32).as_strided(grid, rows, pad),
+                       b.as_strided((n,), (1,), 2 * pad), b.as_strided((E + 1,), (1,), 3 * pad),
+                       b.as_strided(grid, rows, 3 * pad + off))
 
 
 def _check_routing(r: Routing, T: int, k: int, E: int, dev) -> None:
@@ -182,17 +189,24 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     experts left has ids of -1 and weights of 0 behind them.  The result's
     row_index and offsets go to moe_linear, position and weights to
     moe_combine."""
-    _need(logits.dim() == 2, "logits must be a 2-D tensor [T, E]")
+    if logits.dim() != 2:
+        raise ValueError("logits must be a 2-D tensor [T, E]")
     T, E = logits.shape
     dev = logits.device
-    _need(score in _SCORE, f"score is {score!r}, expected 'softmax' or 'sigmoid'")
-    _need(group_score in _GROUP_SCORE, f"group_score is {group_score!r}, expected 'max' or 'top2'")
-    _need(1 <= E <= 512, f"E={E} experts, expected 1 to 512")
-    _need(1 <= groups <= 32 and E % groups == 0, f"groups={groups} must divide E={E} and be at most 32")
-    _need(1 <= topk_groups <= groups, f"topk_groups={topk_groups}, expected 1 to {groups}")
-    _need(1 <= k <= min(32, E // groups * topk_groups),
-          f"k={k}, expected 1 to {min(32, E // groups * topk_groups)}")
-    _need(T * k < 2 ** 31, f"T * k = {T * k} choices, expected below 2^31")
+    if score not in _SCORE:
+        raise ValueError(f"score is {score!r}, expected 'softmax' or 'sigmoid'")
+    if group_score not in _GROUP_SCORE:
+        raise ValueError(f"group_score is {group_score!r}, expected 'max' or 'top2'")
+    if not 1 <= E <= 512:
+        raise ValueError(f"E={E} experts, expected 1 to 512")
+    if not 1 <= groups <= 32 or E % groups:
+        raise ValueError(f"groups={groups} must divide E={E} and be at most 32")
+    if not 1 <= topk_groups <= groups:
+        raise ValueError(f"topk_groups={topk_groups}, expected 1 to {groups}")
+    if not 1 <= k <= min(32, E // groups * topk_groups):
+        raise ValueError(f"k={k}, expected 1 to {min(32, E // groups * topk_groups)}")
+    if T * k >= 2 ** 31:
+        raise ValueError(f"T * k = {T * k} choices, expected below 2^31")
     ld = _rows("logits", logits, (T, E), _BF16_FP32, dev, 2)
     if bias is not None:
         _flat("bias", bias, (E,), _FP32, dev, 4)
@@ -211,11 +225,14 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
 def moe_dispatch(ids, E: int) -> Routing:
     """Dispatch order of given expert ids (int32 [T, k]; outside 0 .. E-1:
     dropped), as moe_route builds it.  The result's weights are None."""
-    _need(ids.dim() == 2, "ids must be a 2-D tensor [T, k]")
+    if ids.dim() != 2:
+        raise ValueError("ids must be a 2-D tensor [T, k]")
     T, k = ids.shape
     dev = ids.device
-    _need(1 <= E <= 512, f"E={E} experts, expected 1 to 512")
-    _need(k >= 1 and T * k < 2 ** 31, f"T * k = {T * k} choices of k={k}, expected k >= 1 and below 2^31")
+    if not 1 <= E <= 512:
+        raise ValueError(f"E={E} experts, expected 1 to 512")
+    if k < 1 or T * k >= 2 ** 31:
+        raise ValueError(f"T * k = {T * k} choices of k={k}, expected k >= 1 and below 2^31")
     _flat("ids", ids, (T, k), _I32, dev, 4)
     i32 = dict(dtype=torch.int32, device=dev)
     r = Routing(ids, None, torch.empty((T * k,), **i32), torch.empty((E + 1,), **i32), torch.empty((T, k), **i32))
@@ -230,14 +247,18 @@ def moe_combine(Y, position, weights, residual=None, out=None):
     Y[position[t, j]] (+ residual[t]).  Y: [rows, N] in dispatch order, bf16
     or fp32; position int32 and weights fp32 [T, k]; residual [T, N] bf16 or
     fp32, which is then the result's type (else Y's).  out may be residual."""
-    _need(Y.dim() == 2, "Y must be a 2-D tensor [rows, N]")
+    if Y.dim() != 2:
+        raise ValueError("Y must be a 2-D tensor [rows, N]")
     rows, N = Y.shape
     dev = Y.device
     _flat("Y", Y, (rows, N), _BF16_FP32, dev)
-    _need(N >= 8 and N % 8 == 0, f"N={N} must be a multiple of 8")
-    _need(isinstance(position, torch.Tensor) and position.dim() == 2, "position must be a 2-D tensor [T, k]")
+    if N < 8 or N % 8:
+        raise ValueError(f"N={N} must be a multiple of 8")
+    if not isinstance(position, torch.Tensor) or position.dim() != 2:
+        raise ValueError("position must be a 2-D tensor [T, k]")
     T, k = position.shape
-    _need(k >= 1, "position must have k >= 1 columns")
+    if k < 1:
+        raise ValueError("position must have k >= 1 columns")
     _flat("position", position, (T, k), _I32, dev, 4)
     _flat("weights", weights, (T, k), _FP32, dev, 4)
     dt = Y.dtype
@@ -293,14 +314,16 @@ def _check_rows8(name: str, q, rows: int, K: int, dev) -> None:
 
 
 def _check_extent(K: int) -> None:
-    _need(8 <= K <= 32768 and K % 8 == 0, f"K={K}, expected a multiple of 8 from 8 to 32768")
+    if not 8 <= K <= 32768 or K % 8:
+        raise ValueError(f"K={K}, expected a multiple of 8 from 8 to 32768")
 
 
 @_placed
 def prepare_int8(X, gamma=None, eps: float = 1e-6, out: Optional[PreparedInt8] = None) -> PreparedInt8:
     """X bf16 [M, K] -> 8-bit codes and a scale for each row, after RMSNorm
     with gamma (bf16 [K]) when it is given."""
-    _need(X.dim() == 2, "X must be a 2-D tensor [M, K]")
+    if X.dim() != 2:
+        raise ValueError("X must be a 2-D tensor [M, K]")
     M, K = X.shape
     dev = X.device
     _check_extent(K)
@@ -308,7 +331,8 @@ def prepare_int8(X, gamma=None, eps: float = 1e-6, out: Optional[PreparedInt8] =
     if gamma is not None:
         _flat("gamma", gamma, (K,), (torch.bfloat16,), dev)
     if out is not None:
-        _need((out.M, out.K) == (M, K), f"out describes M={out.M}, K={out.K}; the call needs M={M}, K={K}")
+        if (out.M, out.K) != (M, K):
+            raise ValueError(f"out describes M={out.M}, K={out.K}; the call needs M={M}, K={K}")
         _check_rows8("out", out, M, K, dev)
     q = out if out is not None else PreparedInt8.empty(M, K, dev)
     c = _RowsInt8(q.codes.data_ptr(), q.scales.data_ptr(), M, K)
@@ -319,14 +343,17 @@ def prepare_int8(X, gamma=None, eps: float = 1e-6, out: Optional[PreparedInt8] =
 @_placed
 def quantize_weight_int8(W, out: Optional[WeightInt8] = None) -> WeightInt8:
     """W bf16 [N, K] -> 8-bit codes and a scale for each output channel."""
-    _need(W.dim() == 2, "W must be a 2-D tensor [N, K]")
+    if W.dim() != 2:
+        raise ValueError("W must be a 2-D tensor [N, K]")
     N, K = W.shape
     dev = W.device
-    _need(N >= 1, "W must have at least one row")
+    if N < 1:
+        raise ValueError("W must have at least one row")
     _check_extent(K)
     _flat("W", W, (N, K), (torch.bfloat16,), dev)
     if out is not None:
-        _need((out.N, out.K) == (N, K), f"out describes N={out.N}, K={out.K}; the call needs N={N}, K={K}")
+        if (out.N, out.K) != (N, K):
+            raise ValueError(f"out describes N={out.N}, K={out.K}; the call needs N={N}, K={K}")
         _check_rows8("out", out, N, K, dev)
     w = out if out is not None else WeightInt8.empty(N, K, dev)
     c = _WeightInt8(w.codes.data_ptr(), w.scales.data_ptr(), N, K)
@@ -340,10 +367,14 @@ def linear_int8(x: PreparedInt8, w: WeightInt8, bias=None, out_fp32: bool = Fals
     sum_k x.codes[i, k] * w.codes[j, k] (+ bias[j]), the sum exact.  bias: bf16
     or fp32 [N]; Y: bf16, or fp32 with out_fp32."""
     dev = x.codes.device
-    _need(isinstance(w, WeightInt8), "w must be a WeightInt8")
-    _need(w.K == x.K, f"weight K={w.K} does not match the activations' K={x.K}")
-    _need(16 <= x.K <= 65536 and x.K % 16 == 0, f"K={x.K}, expected a multiple of 16 from 16 to 65536")
-    _need(w.N >= 1, f"N={w.N}, expected at least 1")
+    if not isinstance(w, WeightInt8):
+        raise ValueError("w must be a WeightInt8")
+    if w.K != x.K:
+        raise ValueError(f"weight K={w.K} does not match the activations' K={x.K}")
+    if not 16 <= x.K <= 65536 or x.K % 16:
+        raise ValueError(f"K={x.K}, expected a multiple of 16 from 16 to 65536")
+    if w.N < 1:
+        raise ValueError(f"N={w.N}, expected at least 1")
     _check_rows8("x", x, x.M, x.K, dev)
     _check_rows8("weight", w, w.N, w.K, dev)
     if bias is not None:
@@ -381,50 +412,65 @@ def residual_norm(x, h=None, norm: Optional[str] = "rms", post_gamma=None, gate=
     strided: the chunks of one modulation tensor), row r of M using row
     r // (M / G).  Returns (x', y): x' in x's type (x itself when h is None),
     y bf16, or a PreparedInt8 with int8=True, or None.  out_x may be x or h."""
-    _need(x.dim() == 2, "x must be a 2-D tensor [M, K]")
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor [M, K]")
     M, K = x.shape
     dev = x.device
     _check_extent(K)
-    _need(norm in _NORM, f"norm is {norm!r}, expected 'rms', 'layer' or None")
+    if norm not in _NORM:
+        raise ValueError(f"norm is {norm!r}, expected 'rms', 'layer' or None")
     a = _ResidualNorm()
     a.ld_x = _rows("x", x, (M, K), _BF16_FP32, dev)
-    if h is None:
-        _need(post_gamma is None and gate is None, "post_gamma and gate need h")
-        _need(norm is not None, "without h and without a norm there is nothing to compute")
-    else:
+    if h is not None:
         a.ld_h = _rows("h", h, (M, K), _BF16_FP32, dev)
-    _need(norm is not None or all(v is None for v in (gamma, beta, scale, shift)),
-          "gamma, beta, scale and shift need a norm")
-    _need(norm is not None or not (int8 or out_y is not None), "int8 and out_y need a norm")
-    vec = [(n, v) for n, v in (("post_gamma", post_gamma), ("gamma", gamma), ("beta", beta)) if v is not None]
-    for n, v in vec:
-        _flat(n, v, (K,), _BF16_FP32, dev)
-        _need(v.dtype == vec[0][1].dtype, f"{n} is {v.dtype}, {vec[0][0]} is {vec[0][1].dtype}")
-    mod = [(n, v) for n, v in (("gate", gate), ("scale", scale), ("shift", shift)) if v is not None]
-    G = 1
-    if mod:
-        _need(mod[0][1].dim() == 2, f"{mod[0][0]} must be a 2-D tensor [G, K]")
-        G = mod[0][1].shape[0]
-        _need(G >= 1 and M % G == 0, f"G={G} rows of {mod[0][0]} must divide M={M}")
-        for n, v in mod:
-            ld = _rows(n, v, (G, K), _BF16_FP32, dev)
-            _need(v.dtype == mod[0][1].dtype, f"{n} is {v.dtype}, {mod[0][0]} is {mod[0][1].dtype}")
-            setattr(a, "ld_" + n, ld)
+        a.h, a.h_is_fp32 = h.data_ptr(), h.dtype == torch.float32
+    elif post_gamma is not None or gate is not None:
+        raise ValueError("post_gamma and gate need h")
+    elif norm is None:
+        raise ValueError("without h and without a norm there is nothing to compute")
+    if norm is None:
+        if gamma is not None or beta is not None or scale is not None or shift is not None:
+            raise ValueError("gamma, beta, scale and shift need a norm")
+        if int8 or out_y is not None:
+            raise ValueError("int8 and out_y need a norm")
+    G, first = 1, None
+    for name, v in (("post_gamma", post_gamma), ("gamma", gamma), ("beta", beta)):
+        if v is not None:
+            _flat(name, v, (K,), _BF16_FP32, dev)
+            first = first or (name, v.dtype)
+            if v.dtype != first[1]:
+                raise ValueError(f"{name} is {v.dtype}, {first[0]} is {first[1]}")
+            setattr(a, name, v.data_ptr())
+    a.norm_is_fp32 = first is not None and first[1] == torch.float32
+    first = None
+    for name, v in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if v is not None:
+            if first is None:
+                if not isinstance(v, torch.Tensor) or v.dim() != 2:
+                    raise ValueError(f"{name} must be a 2-D tensor [G, K]")
+                first, G = (name, v.dtype), v.shape[0]
+                if G < 1 or M % G:
+                    raise ValueError(f"G={G} rows of {name} must divide M={M}")
+            setattr(a, "ld_" + name, _rows(name, v, (G, K), _BF16_FP32, dev))
+            if v.dtype != first[1]:
+                raise ValueError(f"{name} is {v.dtype}, {first[0]} is {first[1]}")
+            setattr(a, name, v.data_ptr())
+    a.mod_is_fp32 = first is not None and first[1] == torch.float32
     if out_x is not None:
         a.ld_out = _rows("out_x", out_x, (M, K), (x.dtype,), dev)
-        for n, v, ld in (("x", x, a.ld_x), ("h", h, a.ld_h)):
-            _need(v is None or v.data_ptr() != out_x.data_ptr() or (ld == a.ld_out and v.dtype == x.dtype),
-                  f"out_x starts where {n} does but has another layout")
+        for name, v, ld in (("x", x, a.ld_x), ("h", h, a.ld_h)):
+            if v is not None and v.data_ptr() == out_x.data_ptr() and (ld != a.ld_out or v.dtype != x.dtype):
+                raise ValueError(f"out_x starts where {name} does but has another layout")
         a.out_x = out_x.data_ptr()
     elif h is not None:
-        out_x = torch.empty((M, K), dtype=x.dtype, device=dev)
+        out_x = torch.empty_like(x, memory_format=torch.contiguous_format)
         a.out_x, a.ld_out = out_x.data_ptr(), K
     y, q = None, None
     if norm is not None:
         if int8:
             if out_y is not None:
-                _need(isinstance(out_y, PreparedInt8) and (out_y.M, out_y.K) == (M, K),
-                      f"out_y must be a PreparedInt8 of M={M}, K={K}")
+                if not isinstance(out_y, PreparedInt8) or (out_y.M, out_y.K) != (M, K):
+                    raise ValueError(f"out_y must be a PreparedInt8 of M={M}, K={K}")
                 _check_rows8("out_y", out_y, M, K, dev)
             y = out_y if out_y is not None else PreparedInt8.empty(M, K, dev)
             q = _RowsInt8(y.codes.data_ptr(), y.scales.data_ptr(), M, K)
@@ -432,15 +478,10 @@ def residual_norm(x, h=None, norm: Optional[str] = "rms", post_gamma=None, gate=
         else:
             if out_y is not None:
                 _flat("out_y", out_y, (M, K), (torch.bfloat16,), dev)
-            y = out_y if out_y is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+            y = out_y if out_y is not None else torch.empty_like(x, dtype=torch.bfloat16,
+                                                                 memory_format=torch.contiguous_format)
             a.y = y.data_ptr()
-    a.x, a.h, a.post_gamma, a.gate = x.data_ptr(), _ptr(h), _ptr(post_gamma), _ptr(gate)
-    a.gamma, a.beta, a.scale, a.shift = _ptr(gamma), _ptr(beta), _ptr(scale), _ptr(shift)
-    a.M, a.G, a.K, a.norm = M, G, K, _NORM[norm]
-    a.x_is_fp32 = x.dtype == torch.float32
-    a.h_is_fp32 = h is not None and h.dtype == torch.float32
-    a.norm_is_fp32 = bool(vec) and vec[0][1].dtype == torch.float32
-    a.mod_is_fp32 = bool(mod) and mod[0][1].dtype == torch.float32
-    a.alpha, a.eps = alpha, eps
+    a.x, a.x_is_fp32 = x.data_ptr(), x.dtype == torch.float32
+    a.M, a.G, a.K, a.norm, a.alpha, a.eps = M, G, K, _NORM[norm], alpha, eps
     _call("sharq_residual_norm", ctypes.byref(a), _stream(dev))
     return out_x if out_x is not None else x, y
