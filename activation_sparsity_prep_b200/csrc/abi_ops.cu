@@ -87,8 +87,9 @@ sharq_status sharq_moe_route(const void* logits, int64_t ld, int logits_fp32, co
     p.sigmoid = opt->score == SHARQ_SCORE_SIGMOID; p.groups = opt->groups; p.topk_groups = opt->topk_groups;
     p.group_top2 = opt->group_score == SHARQ_GROUP_TOP2; p.renormalize = opt->renormalize ? 1 : 0;
     p.scale = opt->scale;
-    const sharq_status st = cuda_status(sharq::launch_route(p, static_cast<cudaStream_t>(stream)));
-    return st != SHARQ_OK || !order ? st : sharq_moe_dispatch(out, stream);
+    const sharq::DispatchLaunch d{out->ids, out->row_index, out->offsets, out->position, out->T * out->k, out->E, out->k};
+    return cuda_status(sharq::launch_route(p, order ? &d : nullptr, static_cast<cudaStream_t>(stream),
+                                           sharq::device_sm_count()));
 }
 
 sharq_status sharq_moe_combine(const void* Y, int y_is_fp32, int64_t rows, int N, const int32_t* position,

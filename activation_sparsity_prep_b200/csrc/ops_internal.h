@@ -41,8 +41,11 @@ struct RouteLaunch {
     int E, k;
     int fp32, sigmoid, groups, topk_groups, group_top2, renormalize;
     float scale;
+    // set by launch_route for its kernels
+    int group_size;
+    int group_whole;            // a group is a power-of-two number of whole lanes
+    int group_shift;            // log2 of the lanes that share a group
 };
-cudaError_t launch_route(const RouteLaunch& p, cudaStream_t s);
 
 struct DispatchLaunch {
     const int32_t* ids;
@@ -53,6 +56,8 @@ struct DispatchLaunch {
     int E, k;
 };
 cudaError_t launch_dispatch(const DispatchLaunch& p, cudaStream_t s);
+// order: also build the dispatch order of the ids written, or null.
+cudaError_t launch_route(const RouteLaunch& p, const DispatchLaunch* order, cudaStream_t s, int sms);
 
 struct CombineLaunch {
     const void* Y;

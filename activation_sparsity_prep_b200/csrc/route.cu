@@ -2,6 +2,9 @@
 // dispatch order that the grouped linear reads, and the weighted sum of the
 // expert outputs back to the tokens (sm_100a).  The formulas are in
 // include/sharq.h.
+#include <algorithm>
+#include <atomic>
+
 #include "common.cuh"
 #include "ops_common.cuh"
 #include "ops_internal.h"
@@ -40,18 +43,77 @@ __device__ __forceinline__ void warp_argmax(double& v, int& e) {
 
 __device__ __forceinline__ float exp_of(float v) { return expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return a < b ? a : b; }
 
-// The choice for one token by one warp; lane l holds experts l, 32 + l, ...
-// (l[j] = -inf where masked).  F = float returns false when two scores that
-// the choice compares lie within the error of their fp32 evaluation; the
-// caller then repeats it in double, so that the experts are those of the
+// Lane i of the warp that routes a token holds experts NPL i .. NPL i + NPL-1:
+// a row is loaded in vectors, and a gather in lane order is in expert order.
+// -inf where masked: beyond E, a logit or a bias of -inf or NaN.
+template <int NPL, bool F32, bool VEC>
+__device__ __forceinline__ void load_logits(const RouteLaunch& a, int64_t t, int lane, float (&l)[NPL]) {
+    const int e0 = lane * NPL;
+    if constexpr (VEC) {
+        constexpr int kBytes = NPL * (F32 ? 4 : 2);
+        uint32_t w[(kBytes + 3) / 4];
+        if (e0 < a.E) {
+            const char* p = static_cast<const char*>(a.logits) + (t * a.ld + e0) * (F32 ? 4 : 2);
+            if constexpr (kBytes >= 16)
+#pragma unroll
+                for (int i = 0; i < kBytes / 16; ++i)
+                    *reinterpret_cast<uint4*>(w + 4 * i) = *reinterpret_cast<const uint4*>(p + 16 * i);
+            else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+            else if constexpr (kBytes == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
+            else w[0] = *reinterpret_cast<const uint16_t*>(p);
+        }
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            const float v = F32 ? __uint_as_float(w[j]) : j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+            l[j] = e0 < a.E ? fmaxf(v, kNegInf) : kNegInf;      // -inf for NaN
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            float v = kNegInf;
+            if (e0 + j < a.E) {
+                const int64_t at = t * a.ld + e0 + j;
+                v = F32 ? static_cast<const float*>(a.logits)[at]
+                        : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at]);
+            }
+            l[j] = fmaxf(v, kNegInf);
+        }
+    }
+}
+
+// The biases of a lane's experts, -inf where they mask; whether any does.
+template <int NPL>
+__device__ __forceinline__ bool load_bias(const RouteLaunch& a, int lane, float (&b)[NPL]) {
+    bool masks = false;
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+        b[j] = fmaxf(a.bias && lane * NPL + j < a.E ? a.bias[lane * NPL + j] : 0.0f, kNegInf);
+        masks |= !(b[j] > kNegInf);
+    }
+    return __any_sync(kFull, masks);
+}
+
+// The choice for one token by one warp, a search round for each expert.
+// F = float returns false when two scores that the choice compares lie within
+// the error of their fp32 evaluation, or the chosen scores' sum underflows;
+// the caller then repeats it in double, so that the experts are those of the
 // formula and not of its rounding.  Without a bias the scores' order is that
 // of the logits, which needs no evaluation.
-template <int NPL, typename F>
-__device__ bool choose(const float (&l)[NPL], const float (&b)[NPL], const RouteLaunch& a, int lane,
-                       F* scratch, int& id_out, float& w_out) {
+template <int NPL, bool F32, typename F>
+__device__ bool choose(const RouteLaunch& a, int64_t t, int lane, F* scratch) {
     constexpr bool kFp32 = sizeof(F) == 4;
+    float l[NPL], b[NPL];
+    load_logits<NPL, F32, false>(a, t, lane, l);
+    load_bias(a, lane, b);
     F s[NPL], key[NPL];
+#pragma unroll
+    for (int j = 0; j < NPL; ++j)
+        if (!(b[j] > kNegInf)) l[j] = kNegInf;
     // |error| of an fp32 score: a relative part from exp, sum and quotient,
     // an absolute one from rounding score + bias
     const float rel = a.sigmoid ? 4.8e-7f : 1.9e-6f;      // 2^-21, 2^-19
@@ -85,7 +147,7 @@ __device__ bool choose(const float (&l)[NPL], const float (&b)[NPL], const Route
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-            const int e = j * 32 + lane;
+            const int e = lane * NPL + j;
             if (e < a.E)
                 scratch[e] = a.group_top2 && !scored ? (l[j] > kNegInf ? s[j] : F(kNegInf)) : key[j];
         }
@@ -118,12 +180,9 @@ __device__ bool choose(const float (&l)[NPL], const float (&b)[NPL], const Route
             last = v;
             if (lane == g) top = F(kNegInf);
         }
-        const uint32_t recip = ((1u << 20) + gs - 1) / gs;      // e * recip >> 20 == e / gs below 512
 #pragma unroll
-        for (int j = 0; j < NPL; ++j) {
-            const uint32_t g = (uint32_t)(j * 32 + lane) * recip >> 20;
-            if (!(chosen >> (g & 31) & 1u)) key[j] = F(kNegInf);
-        }
+        for (int j = 0; j < NPL; ++j)
+            if (!(chosen >> ((lane * NPL + j) / gs & 31) & 1u)) key[j] = F(kNegInf);
     }
 
     int id = -1;
@@ -131,17 +190,17 @@ __device__ bool choose(const float (&l)[NPL], const float (&b)[NPL], const Route
     const int rounds = kFp32 && scored ? a.k + 1 : a.k;         // one more to see the gap behind the last
     for (int r = 0; r < rounds; ++r) {
         F v = key[0];
-        int e = lane;
+        int e = lane * NPL;
 #pragma unroll
         for (int j = 1; j < NPL; ++j)
-            if (key[j] > v) { v = key[j]; e = j * 32 + lane; }
+            if (key[j] > v) { v = key[j]; e = lane * NPL + j; }
         warp_argmax(v, e);
         if (!(v > F(kNegInf))) break;
         F sv = 0;
 #pragma unroll
         for (int j = 0; j < NPL; ++j)
-            if (j * 32 + lane == e) { sv = s[j]; key[j] = F(kNegInf); }
-        sv = __shfl_sync(kFull, sv, e & 31);
+            if (lane * NPL + j == e) { sv = s[j]; key[j] = F(kNegInf); }
+        sv = __shfl_sync(kFull, sv, e / NPL);
         if (kFp32 && scored && r > 0 &&
             prev - v <= F(2.0f * rel * fmaxf((float)prev_s, (float)sv) + 2.4e-7f * (1.0f + fmaxf(fabsf((float)prev), fabsf((float)v)))))
             return false;
@@ -151,53 +210,313 @@ __device__ bool choose(const float (&l)[NPL], const float (&b)[NPL], const Route
     }
     if (a.renormalize) {
         const F sum = warp_sum(w);
+        if (kFp32 && sum < F(1e-30f) && __any_sync(kFull, id >= 0)) return false;
         w = sum > F(0) ? w / sum : F(0);
     }
-    id_out = id;
-    w_out = (float)(w * F(a.scale));
+    if (lane < a.k) {
+        a.ids[t * a.k + lane] = id;
+        a.weights[t * a.k + lane] = (float)(w * F(a.scale));
+    }
     return true;
 }
 
-// One warp a token.
-template <int NPL, bool F32>
-__global__ void __launch_bounds__(kRouteWarps * 32)
-route_kernel(const RouteLaunch a) {
-    extern __shared__ double route_smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
-    if (t >= a.T) return;
-    double* scratch = route_smem + warp * a.E;
-    float l[NPL], b[NPL];
-#pragma unroll
-    for (int j = 0; j < NPL; ++j) {
-        const int e = j * 32 + lane;
-        float v = kNegInf, w = 0.0f;
-        if (e < a.E) {
-            if (F32) v = static_cast<const float*>(a.logits)[t * a.ld + e];
-            else     v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[t * a.ld + e]);
-            if (a.bias) w = a.bias[e];
-        }
-        const bool live = v > kNegInf && w > kNegInf;           // false for NaN too
-        l[j] = live ? v : kNegInf;
-        b[j] = live ? w : 0.0f;
-    }
-    int id;
-    float w;
-    if (!choose<NPL, float>(l, b, a, lane, reinterpret_cast<float*>(scratch), id, w))
-        choose<NPL, double>(l, b, a, lane, scratch, id, w);
-    if (lane < a.k) {
-        a.ids[t * a.k + lane] = id;
-        a.weights[t * a.k + lane] = w;
-    }
+// Per-warp shared memory of the fast choice.
+struct RouteScratch {
+    double key[36];                      // floats in the fp32 form; padded to a multiple of four
+    int expert[32];
+};
+
+// Largest value over the warp.
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
-template <int NPL>
-cudaError_t launch_route_n(const RouteLaunch& p, cudaStream_t s) {
-    const unsigned grid = (unsigned)((p.T + kRouteWarps - 1) / kRouteWarps);
-    const size_t smem = p.groups > 1 ? (size_t)kRouteWarps * p.E * sizeof(double) : 0;
-    if (p.fp32) route_kernel<NPL, true><<<grid, kRouteWarps * 32, smem, s>>>(p);
-    else        route_kernel<NPL, false><<<grid, kRouteWarps * 32, smem, s>>>(p);
-    return cudaGetLastError();
+__device__ __forceinline__ float fast_exp(float v) {           // ex2.approx: 2^-22 + |v| 2^-23 relative
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+    return r;
+}
+__device__ __forceinline__ double fast_exp(double v) { return exp(v); }
+__device__ __forceinline__ float quotient(float a, float b) { return __fdividef(a, b); }
+__device__ __forceinline__ double quotient(double a, double b) { return a / b; }
+
+// Masks the keys outside the groups that a token may use; `of` holds what a
+// group's score is made of.  Returns false when the last kept and the first
+// dropped group are too close for fp32 (checked where scores are inexact).
+// 1 << group_shift lanes share a group: where a group is a power-of-two
+// number of whole lanes from their registers, else through shared memory,
+// each lane reading every p-th of the group's experts.
+template <int NPL, typename F>
+__device__ __forceinline__ bool keep_groups(const F (&of)[NPL], F (&key)[NPL], const RouteLaunch& a, int lane,
+                                            bool inexact, float rel, F* scratch) {
+    F top = F(kNegInf), second = F(kNegInf);
+    const int p = 1 << a.group_shift, g = lane >> a.group_shift;
+    if (a.group_whole) {
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            second = larger(second, smaller(top, of[j]));
+            top = larger(top, of[j]);
+        }
+    } else {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < NPL; ++j)
+            if (lane * NPL + j < a.E) scratch[lane * NPL + j] = of[j];
+        __syncwarp();
+        const int gs = a.group_size, sub = lane & (p - 1);
+        if (g < a.groups) {
+            const int n = (gs + p - 1) >> a.group_shift;
+            int it = g % n;                               // rotated start: groups would share a bank
+            for (int i = 0; i < n; ++i) {
+                const int at = (it << a.group_shift) + sub;
+                const F v = at < gs ? scratch[g * gs + at] : F(kNegInf);
+                it = it + 1 == n ? 0 : it + 1;
+                second = larger(second, smaller(top, v));
+                top = larger(top, v);
+            }
+        }
+    }
+    for (int o = 1; o < p; o <<= 1) {
+        const F t = __shfl_xor_sync(kFull, top, o), u = __shfl_xor_sync(kFull, second, o);
+        second = larger(smaller(top, t), larger(second, u));
+        top = larger(top, t);
+    }
+    if (a.group_top2 && second > F(kNegInf)) top += second;
+    if (g >= a.groups) top = F(kNegInf);
+    // rank of this lane's group, equal groups by index
+    int rank = 0;
+#pragma unroll 4
+    for (int h = 0; h < a.groups; ++h) {
+        const F v = __shfl_sync(kFull, top, h << a.group_shift);
+        rank += v > top || (v == top && h < g);
+    }
+    const bool live = top > F(kNegInf);
+    const bool kept = live && rank < a.topk_groups;
+    if (sizeof(F) == 4 && inexact) {
+        const float worst = -redux_max(kept ? -(float)top : kNegInf);
+        const float best = redux_max(live && !kept ? (float)top : kNegInf);
+        if (worst - best <= 4.0f * (2.0f * rel + 2.4e-7f * (1.0f + fabsf(worst)))) return false;
+    }
+    if (a.group_whole) {
+#pragma unroll
+        for (int j = 0; j < NPL; ++j)
+            if (!kept) key[j] = F(kNegInf);
+    } else {
+        const uint32_t lanes = __ballot_sync(kFull, kept);
+        const uint32_t recip = ((1u << 20) + a.group_size - 1) / a.group_size;      // e * recip >> 20 == e / size below 512
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            const uint32_t h = (uint32_t)(lane * NPL + j) * recip >> 20;
+            if (!(lanes >> ((h << a.group_shift) & 31) & 1u)) key[j] = F(kNegInf);
+        }
+    }
+    return true;
+}
+
+enum Choice { kChosen, kTooClose, kTooMany };
+
+// The choice without a search round for each expert.  The k-th largest of the
+// 32 lane maxima bounds the k-th largest key from below, so the few keys not
+// under it are gathered, in expert order, and ranked against one another.
+// The kernel is bound by instruction issue: 16383 tokens of 256 experts took
+// 13.8 M warp instructions and 25 us with search rounds (sigmoid with bias).
+// F = float leaves close decisions to F = double (kTooClose), which gathers
+// on its keys rounded to fp32, an order-preserving step, and ranks the keys
+// themselves.  Nothing is written unless kChosen is returned.
+template <int NPL, bool F32, bool VEC, typename F>
+__device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, int lane, const float (&b)[NPL],
+                                              bool bias_masks, F* scratch, RouteScratch& sh) {
+    constexpr bool kFp32 = sizeof(F) == 4;
+    const bool scored = a.bias != nullptr;
+    const bool need_all = scored || (a.groups > 1 && a.group_top2);      // every score, not just the chosen ones'
+    const float rel = a.sigmoid ? 4.8e-7f : 1.9e-6f;                     // see choose(); the fast exponential is within both
+    F key[NPL];
+    F m = 0, r = 1;
+    {
+        float l[NPL];
+        load_logits<NPL, F32, VEC>(a, t, lane, l);
+        if (bias_masks)
+#pragma unroll
+            for (int j = 0; j < NPL; ++j)
+                if (!(b[j] > kNegInf)) l[j] = kNegInf;
+        if (!a.sigmoid && (need_all || !a.renormalize)) {
+            float top = l[0];
+#pragma unroll
+            for (int j = 1; j < NPL; ++j) top = fmaxf(top, l[j]);
+            top = redux_max(top);
+            m = top > kNegInf ? top : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) key[j] = l[j];
+    }
+    if (need_all) {
+        F s[NPL];
+        if (a.sigmoid) {
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) s[j] = quotient(F(1), F(1) + fast_exp(-key[j]));
+        } else {
+            F sum = 0;
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) {
+                s[j] = fast_exp(key[j] - m);
+                sum += s[j];
+            }
+            sum = warp_sum(sum);
+            r = sum > F(0) ? quotient(F(1), sum) : F(0);
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) s[j] *= r;
+        }
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            s[j] = key[j] > F(kNegInf) ? s[j] + F(b[j]) : F(kNegInf);    // b is 0 without a bias
+            if (scored) key[j] = s[j];
+        }
+        if (a.groups > 1 && !keep_groups(s, key, a, lane, true, rel, scratch)) return kTooClose;
+    } else {
+        if (!a.sigmoid && !a.renormalize) {
+            F sum = 0;
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) sum += exp_of(key[j] - m);     // 0 where masked
+            sum = warp_sum(sum);
+            r = sum > F(0) ? quotient(F(1), sum) : F(0);
+        }
+        if (a.groups > 1) keep_groups(key, key, a, lane, false, rel, scratch);
+    }
+
+    // the bound: one more than k where the gap behind the last choice counts
+    float top = (float)key[0];
+#pragma unroll
+    for (int j = 1; j < NPL; ++j) top = fmaxf(top, (float)key[j]);
+    float bound = kNegInf;
+    const int rounds = scored ? a.k + 1 : a.k;
+#pragma unroll 2
+    for (int i = 0; i < rounds; ++i) {
+        bound = redux_max(top);
+        if (top == bound) top = kNegInf;                  // lanes with equal maxima go together: a lower bound still
+    }
+    bound = fmaxf(bound, -3.4028235e38f);                 // masked keys stay out
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) n += (float)key[j] >= bound;
+    int at = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, at, o);
+        if (lane >= o) at += u;
+    }
+    const int count = __shfl_sync(kFull, at, 31);
+    if (count > 32) return kTooMany;
+    at -= n;
+    F* gathered = reinterpret_cast<F*>(sh.key);
+    __syncwarp();                                         // the previous token's reads are done
+    if (n) {
+#pragma unroll
+        for (int j = 0; j < NPL; ++j)
+            if ((float)key[j] >= bound) {
+                gathered[at] = key[j];
+                sh.expert[at] = lane * NPL + j;
+                ++at;
+            }
+    }
+    if (lane < 4) gathered[count + lane] = F(kNegInf);
+    __syncwarp();
+    const bool mine = lane < count;
+    const F v = mine ? gathered[lane] : F(kNegInf);
+    const int e = mine ? sh.expert[lane] : 0;
+    int rank = 0;
+    if constexpr (kFp32) {
+        for (int i = 0; i < count; i += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(gathered + i);
+            rank += (w.x > v) + (w.y > v) + (w.z > v) + (w.w > v);
+        }
+        // equal keys (both zeros alike): the lower index first
+        rank += __popc(__match_any_sync(kFull, __float_as_uint(v + 0.0f)) & ((1u << lane) - 1u));
+    } else {
+        for (int i = 0; i < count; ++i) rank += gathered[i] > v || (gathered[i] == v && i < lane);
+    }
+    const bool chosen = mine && rank < a.k;
+    F x = v;
+    if (scored && mine)
+        x = F32 ? static_cast<const float*>(a.logits)[t * a.ld + e]
+                : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[t * a.ld + e]);
+    F score;
+    if (a.sigmoid) {
+        score = quotient(F(1), F(1) + exp_of(-x));
+    } else {
+        // the sum over all experts cancels where weights are renormalised
+        F c = m;
+        if (a.renormalize) {
+            c = F(redux_max(chosen ? (float)x : kNegInf));
+            if (kFp32 && need_all && c - m < F(-80)) return kTooClose;
+            if (!kFp32 && need_all && exp_of(c - m) == F(0)) r = 0;      // every chosen score is 0
+        }
+        score = exp_of(x - c) * (!a.renormalize || r == F(0) ? r : F(1));
+    }
+    if (kFp32 && scored) {
+        // neighbours in rank order; a score is at most 1
+        __syncwarp();
+        if (mine) gathered[rank] = v;
+        __syncwarp();
+        bool close = false;
+        if (lane < a.k && lane + 1 < count) {
+            const float p = (float)gathered[lane], q = (float)gathered[lane + 1];
+            close = p - q <= 2.0f * rel + 2.4e-7f * (1.0f + fmaxf(fabsf(p), fabsf(q)));
+        }
+        if (__any_sync(kFull, close)) return kTooClose;
+    }
+    F w = chosen ? score : F(0);
+    if (a.renormalize) {
+        const F sum = warp_sum(w);
+        if (kFp32 && sum < F(1e-30f) && count > 0) return kTooClose;
+        w = sum > F(0) ? quotient(w, sum) : F(0);
+    }
+    const int64_t to = t * a.k;
+    if (chosen) {
+        a.ids[to + rank] = e;
+        a.weights[to + rank] = (float)(w * F(a.scale));
+    }
+    if (lane >= count && lane < a.k) {
+        a.ids[to + lane] = -1;
+        a.weights[to + lane] = 0.0f;
+    }
+    return kChosen;
+}
+
+// What the fp32 form leaves undecided.  Not inlined: its registers (the scores
+// in double) would halve the resident warps of the fp32 form.
+template <int NPL, bool F32>
+__device__ __noinline__ void choose_slow(const RouteLaunch* a, int64_t t, int lane, Choice why, double* scratch,
+                                         RouteScratch* sh) {
+    if (why == kTooClose) {
+        float b[NPL];
+        const bool masks = load_bias(*a, lane, b);
+        why = choose_fast<NPL, F32, false>(*a, t, lane, b, masks, scratch, *sh);
+    }
+    if (why == kTooMany && !choose<NPL, F32>(*a, t, lane, reinterpret_cast<float*>(scratch)))
+        choose<NPL, F32>(*a, t, lane, scratch);
+}
+
+// One warp routes token t.  scratch: E doubles of this warp.
+template <int NPL, bool F32, bool VEC>
+__device__ __forceinline__ void route_token(const RouteLaunch& a, int64_t t, int lane, const float (&b)[NPL],
+                                            bool bias_masks, double* scratch, RouteScratch& sh) {
+    const Choice c = choose_fast<NPL, F32, VEC>(a, t, lane, b, bias_masks, reinterpret_cast<float*>(scratch), sh);
+    if (c != kChosen) choose_slow<NPL, F32>(&a, t, lane, c, scratch, &sh);
+}
+
+// One warp a token, a warp walking several.
+template <int NPL, bool F32, bool VEC>
+__global__ void __launch_bounds__(kRouteWarps * 32, NPL <= 8 ? 4 : 2)
+route_kernel(const __grid_constant__ RouteLaunch a) {
+    extern __shared__ double route_smem[];
+    __shared__ alignas(16) RouteScratch sh[kRouteWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float b[NPL];
+    const bool masks = load_bias(a, lane, b);
+    for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.T; t += (int64_t)gridDim.x * kRouteWarps)
+        route_token<NPL, F32, VEC>(a, t, lane, b, masks, route_smem + warp * a.E, sh[warp]);
 }
 
 // ---------------------------------------------------------- dispatch ------
@@ -206,17 +525,52 @@ cudaError_t launch_route_n(const RouteLaunch& p, cudaStream_t s) {
 // memory; the rows are scanned over the block's warps, the block totals over
 // the cluster (distributed shared memory) and the experts, and a second walk
 // over the same run places each choice.  Equal ids inside a group of 32 are
-// ranked by a warp match.  No workspace, no atomics: the order is fixed.
+// ranked by a warp match, so the order is fixed; no workspace.
 constexpr int kDispWarps = 32;
+constexpr int kBatch = 8;            // groups of 32 choices whose loads are in flight together
 
+// ids[first + 32 b + lane], -1 where there is none or no such expert
+__device__ __forceinline__ void load_batch(const DispatchLaunch& a, int64_t at, int64_t end, int lane, int (&e)[kBatch]) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+        const int64_t i = at + b * 32 + lane;
+        e[b] = i < end ? a.ids[i] : -1;
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+        if ((unsigned)e[b] >= (unsigned)a.E) e[b] = -1;
+}
+
+// Exclusive scan of v over the block's 1024 threads; sum: the total.
+__device__ __forceinline__ int block_scan(int v, int* wsum, int& sum) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int w = wsum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, w, o);
+        if (lane >= o) w += u;
+    }
+    sum = __shfl_sync(kFull, w, 31);
+    const int before = warp ? __shfl_sync(kFull, w, warp - 1) : 0;
+    return before + inc - v;
+}
+
+// C blocks share the choices; with C == 1 the block also writes row_index,
+// with more the scatter is left to invert_kernel, which has every SM's store
+// units (8 blocks alone took 9 us for 131072 rows).
 template <int C>
-__global__ void __launch_bounds__(kDispWarps * 32)
-dispatch_kernel(const DispatchLaunch a) {
-    extern __shared__ int disp_smem[];
-    int* hist = disp_smem;                        // [kDispWarps][E]
+__device__ __forceinline__ void dispatch_body(const DispatchLaunch& a, int* smem, int* wsum) {
+    int* hist = smem;                             // [kDispWarps][E]
     int* total = hist + kDispWarps * a.E;         // [E] this block's counts
     int* start = total + a.E;                     // [E] first slot of this block's rows
-    __shared__ int wsum[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = C > 1 ? (int)cluster_ctarank() : 0;
     const int64_t per = (a.n + (int64_t)C * kDispWarps * 32 - 1) / ((int64_t)C * kDispWarps * 32) * 32;
@@ -226,17 +580,18 @@ dispatch_kernel(const DispatchLaunch a) {
 
     for (int i = threadIdx.x; i < kDispWarps * a.E; i += blockDim.x) hist[i] = 0;
     __syncthreads();
-    for (int64_t i = first + lane; i - lane < end; i += 32) {
-        const int e = i < end ? a.ids[i] : -1;
-        const bool ok = e >= 0 && e < a.E;
-        const unsigned peers = __match_any_sync(kFull, ok ? e : -1);
-        if (ok && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-        __syncwarp();
+    for (int64_t at = first; at < end; at += kBatch * 32) {
+        int e[kBatch];
+        load_batch(a, at, end, lane, e);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (e[b] >= 0) atomicAdd(&mine[e[b]], 1);     // counts only: their order does not matter
     }
     __syncthreads();
     // exclusive scan of each expert's counts over the block's warps
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         int sum = 0;
+#pragma unroll 8
         for (int w = 0; w < kDispWarps; ++w) {
             const int v = hist[w * a.E + e];
             hist[w * a.E + e] = sum;
@@ -248,63 +603,105 @@ dispatch_kernel(const DispatchLaunch a) {
     else       __syncthreads();
     // experts' first slots: exclusive scan over the experts (E <= blockDim)
     int all = 0, before = 0;
-    const int e = threadIdx.x;
-    if (e < a.E) {
+    const int x = threadIdx.x;
+    if (x < a.E) {
+#pragma unroll
         for (int r = 0; r < C; ++r) {
-            const int v = C > 1 ? __float_as_int(ld_shared_cluster_f32(&total[e], r)) : total[e];
+            const int v = C > 1 ? __float_as_int(ld_shared_cluster_f32(&total[x], r)) : total[x];
             if (r < rank) before += v;
             all += v;
         }
     }
-    int inc = all;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += v;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int base = 0;
-    for (int w = 0; w < warp; ++w) base += wsum[w];
-    int live = 0;
-    for (int w = 0; w < kDispWarps; ++w) live += wsum[w];
-    if (e < a.E) {
-        start[e] = base + inc - all + before;
-        if (rank == 0) a.offsets[e] = base + inc - all;
+    int live;
+    const int base = block_scan(all, wsum, live);
+    if (x < a.E) {
+        start[x] = base + before;
+        if (rank == 0) a.offsets[x] = base;
     }
     if (rank == 0 && threadIdx.x == 0) a.offsets[a.E] = live;
     __syncthreads();
-    for (int64_t i = first + lane; i - lane < end; i += 32) {
-        const int e2 = i < end ? a.ids[i] : -1;
-        const bool ok = e2 >= 0 && e2 < a.E;
-        const unsigned peers = __match_any_sync(kFull, ok ? e2 : -1);
-        int at = 0;
-        if (ok) at = start[e2] + mine[e2] + __popc(peers & ((1u << lane) - 1u));
-        __syncwarp();
-        if (ok && lane == __ffs(peers) - 1) mine[e2] += __popc(peers);
-        __syncwarp();
-        if (i < end) {
-            a.position[i] = ok ? at : -1;
-            if (ok) a.row_index[at] = (int)(i / a.k);
+    for (int64_t at = first; at < end; at += kBatch * 32) {
+        int e[kBatch];
+        load_batch(a, at, end, lane, e);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t i = at + b * 32 + lane;
+            const unsigned peers = __match_any_sync(kFull, e[b]);
+            int slot = -1;
+            if (e[b] >= 0) slot = start[e[b]] + mine[e[b]] + __popc(peers & ((1u << lane) - 1u));
+            __syncwarp();
+            if (e[b] >= 0 && lane == __ffs(peers) - 1) mine[e[b]] += __popc(peers);
+            __syncwarp();
+            if (i < end) {
+                a.position[i] = slot;
+                if (C == 1 && slot >= 0) a.row_index[slot] = (int)((uint32_t)i / (uint32_t)a.k);
+            }
         }
     }
     // slots behind the last live one name row 0: valid rows of no expert
-    for (int64_t i = live + (int64_t)rank * blockDim.x + threadIdx.x; i < a.n; i += (int64_t)C * blockDim.x)
-        a.row_index[i] = 0;
+    if (C == 1)
+        for (int64_t i = live + threadIdx.x; i < a.n; i += blockDim.x) a.row_index[i] = 0;
     if (C > 1) cluster_sync_all();                // no block leaves while its totals are read
 }
 
 template <int C>
+__global__ void __launch_bounds__(kDispWarps * 32)
+dispatch_kernel(const DispatchLaunch a) {
+    extern __shared__ int disp_smem[];
+    __shared__ int wsum[32];
+    dispatch_body<C>(a, disp_smem, wsum);
+}
+
+__global__ void __launch_bounds__(256)
+invert_kernel(const DispatchLaunch a) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.n) return;
+    const int slot = a.position[i];
+    if (slot >= 0) a.row_index[slot] = (int)((uint32_t)i / (uint32_t)a.k);
+    if (i >= a.offsets[a.E]) a.row_index[i] = 0;
+}
+
+// Few tokens: the choice and the dispatch order by one block, in one launch.
+constexpr int kFusedTokens = 64;
+
+template <int NPL, bool F32, bool VEC>
+__global__ void __launch_bounds__(kDispWarps * 32)
+route_dispatch_kernel(const __grid_constant__ RouteLaunch r, const DispatchLaunch d) {
+    extern __shared__ double route_smem[];
+    __shared__ alignas(16) RouteScratch sh[kDispWarps];
+    __shared__ int wsum[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float b[NPL];
+    const bool masks = load_bias(r, lane, b);
+    for (int64_t t = warp; t < r.T; t += kDispWarps)
+        route_token<NPL, F32, VEC>(r, t, lane, b, masks, route_smem + warp * r.E, sh[warp]);
+    __syncthreads();                              // the block's own ids, written to global memory, are read back
+    dispatch_body<1>(d, reinterpret_cast<int*>(route_smem), wsum);
+}
+
+template <class Fn>
+cudaError_t allow_smem(std::atomic<bool> (&done)[64], Fn kernel, size_t bytes, bool wide_cluster = false) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && wide_cluster)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+constexpr size_t dispatch_smem(int E) { return (size_t)(kDispWarps + 2) * E * sizeof(int); }
+
+template <int C>
 cudaError_t launch_dispatch_c(const DispatchLaunch& p, cudaStream_t s) {
-    const size_t smem = (size_t)(kDispWarps + 2) * p.E * sizeof(int);
-    if (cudaError_t e = cudaFuncSetAttribute(dispatch_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)((kDispWarps + 2) * kMaxRouteExperts * sizeof(int)));
-        e != cudaSuccess)
+    static std::atomic<bool> done[64];
+    if (cudaError_t e = allow_smem(done, dispatch_kernel<C>, dispatch_smem(kMaxRouteExperts), C > 8); e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C);
     cfg.blockDim = dim3(kDispWarps * 32);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = dispatch_smem(p.E);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -314,6 +711,41 @@ cudaError_t launch_dispatch_c(const DispatchLaunch& p, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, dispatch_kernel<C>, p);
+}
+
+template <int NPL, bool F32, bool VEC>
+cudaError_t launch_route_v(const RouteLaunch& p, const DispatchLaunch* order, cudaStream_t s, int sms) {
+    if (order && p.T <= kFusedTokens) {
+        // scratch of 32 warps and, later, the histograms
+        const size_t smem = std::max((size_t)kDispWarps * p.E * sizeof(double), dispatch_smem(p.E));
+        static std::atomic<bool> done[64];
+        if (cudaError_t e = allow_smem(done, route_dispatch_kernel<NPL, F32, VEC>,
+                                       (size_t)kDispWarps * kMaxRouteExperts * sizeof(double));
+            e != cudaSuccess)
+            return e;
+        route_dispatch_kernel<NPL, F32, VEC><<<1, kDispWarps * 32, smem, s>>>(p, *order);
+        return cudaGetLastError();
+    }
+    const int64_t blocks = std::min<int64_t>((p.T + kRouteWarps - 1) / kRouteWarps, (int64_t)sms * 12);
+    const size_t smem = p.groups > 1 ? (size_t)kRouteWarps * p.E * sizeof(double) : 0;
+    route_kernel<NPL, F32, VEC><<<(unsigned)blocks, kRouteWarps * 32, smem, s>>>(p);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    return order ? launch_dispatch(*order, s) : cudaSuccess;
+}
+
+template <int NPL>
+cudaError_t launch_route_n(const RouteLaunch& given, const DispatchLaunch* order, cudaStream_t s, int sms) {
+    RouteLaunch p = given;
+    p.group_size = p.E / p.groups;
+    const int lanes = p.group_size / NPL;
+    p.group_whole = p.group_size % NPL == 0 && (lanes & (lanes - 1)) == 0;
+    const int most = p.group_whole ? lanes : 32 / p.groups;
+    while ((2 << p.group_shift) <= most) ++p.group_shift;
+    // whole lanes of experts, every lane's first on a boundary of its vector
+    const int size = p.fp32 ? 4 : 2, align = std::min(16, NPL * size);
+    const bool vec = p.E % NPL == 0 && p.ld * size % align == 0 && reinterpret_cast<uintptr_t>(p.logits) % align == 0;
+    if (p.fp32) return vec ? launch_route_v<NPL, true, true>(p, order, s, sms) : launch_route_v<NPL, true, false>(p, order, s, sms);
+    return vec ? launch_route_v<NPL, false, true>(p, order, s, sms) : launch_route_v<NPL, false, false>(p, order, s, sms);
 }
 
 // ----------------------------------------------------------- combine ------
@@ -362,18 +794,23 @@ combine_kernel(const CombineLaunch a) {
 
 }  // namespace
 
-cudaError_t launch_route(const RouteLaunch& p, cudaStream_t s) {
-    if (p.T == 0) return cudaSuccess;
-    if (p.E <= 32) return launch_route_n<1>(p, s);
-    if (p.E <= 64) return launch_route_n<2>(p, s);
-    if (p.E <= 128) return launch_route_n<4>(p, s);
-    if (p.E <= 256) return launch_route_n<8>(p, s);
-    return launch_route_n<16>(p, s);
+cudaError_t launch_route(const RouteLaunch& p, const DispatchLaunch* order, cudaStream_t s, int sms) {
+    if (p.T == 0) return order ? launch_dispatch(*order, s) : cudaSuccess;
+    if (p.E <= 32) return launch_route_n<1>(p, order, s, sms);
+    if (p.E <= 64) return launch_route_n<2>(p, order, s, sms);
+    if (p.E <= 128) return launch_route_n<4>(p, order, s, sms);
+    if (p.E <= 256) return launch_route_n<8>(p, order, s, sms);
+    return launch_route_n<16>(p, order, s, sms);
 }
 
 cudaError_t launch_dispatch(const DispatchLaunch& p, cudaStream_t s) {
-    // one block covers 4 choices a thread; beyond that a cluster of 8
-    return p.n <= 4096 ? launch_dispatch_c<1>(p, s) : launch_dispatch_c<8>(p, s);
+    // one block covers up to 4 choices a thread; beyond that a cluster does,
+    // of 16 blocks where the device places one
+    if (p.n <= 4096) return launch_dispatch_c<1>(p, s);
+    cudaError_t e = p.n > 8 * 4096 ? launch_dispatch_c<16>(p, s) : launch_dispatch_c<8>(p, s);
+    if (e != cudaSuccess) return e;
+    invert_kernel<<<(unsigned)((p.n + 255) / 256), 256, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_combine(const CombineLaunch& p, cudaStream_t s) {

@@ -365,7 +365,8 @@ typedef struct {
  *   renormalize is set (0 when that sum is 0), times scale.
  * The comparisons decide as they would in 64-bit arithmetic: scores that
  * fp32 cannot tell apart are evaluated again in double.  A softmax over a
- * logit of +inf has no value: its weights are NaN.
+ * logit of +inf has no value: that token's ids (in -1 .. E-1) and weights are
+ * unspecified.
  * 1 <= E <= 512, E a multiple of groups, 1 <= k <= 32, k at most the experts
  * of topk_groups groups, T * k < 2^31.  When out->row_index is not NULL the
  * dispatch order is built too, as sharq_moe_dispatch. */
