@@ -284,7 +284,8 @@ sharq_status sharq_last_device_status(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return SHARQ_ERR_CUDA;
     unsigned v = sharq::take_status_prepare() | sharq::take_status_linear() |
-                 sharq::take_status_selftest() | sharq::take_status_int8();
+                 sharq::take_status_selftest() | sharq::take_status_int8() |
+                 sharq::take_status_norm();
     if (v & sharq::kStatusReadFailed) return SHARQ_ERR_CUDA;
     if (v & (sharq::kStatusGridTimeout | sharq::kStatusMbarTimeout)) return SHARQ_ERR_TIMEOUT;
     if (v) return SHARQ_ERR_CUDA;

@@ -45,10 +45,10 @@ sharq_status quantize_rows(const void* X, const void* gamma, float eps, int8_t* 
         return SHARQ_ERR_INVALID_ARG;
     if ((M > 0 && !X) || !aligned(X, 16) || !aligned(gamma, 16)) return SHARQ_ERR_INVALID_ARG;
     sharq::NormLaunch p{};
-    p.x = X; p.ldx = K; p.M = M; p.K = K; p.group_rows = 1;
+    p.x = X; p.ldx = K; p.M = M; p.K = K; p.group_rows = M;
     p.gamma = gamma; p.norm = gamma ? SHARQ_NORM_RMS : SHARQ_NORM_NONE; p.eps = eps;
     p.codes = codes; p.row_scale = scales;
-    return cuda_status(sharq::launch_residual_norm(p, static_cast<cudaStream_t>(stream)));
+    return cuda_status(sharq::launch_residual_norm(p, static_cast<cudaStream_t>(stream), sharq::device_sm_count()));
 }
 
 }  // namespace
@@ -132,7 +132,7 @@ sharq_status sharq_residual_norm(const sharq_residual_norm_args* a, void* stream
     p.ldo = a->ld_out; p.M = a->M; p.group_rows = a->M / a->G; p.K = a->K; p.norm = a->norm;
     p.x_fp32 = a->x_is_fp32 ? 1 : 0; p.h_fp32 = a->h_is_fp32 ? 1 : 0; p.norm_fp32 = a->norm_is_fp32 ? 1 : 0;
     p.mod_fp32 = a->mod_is_fp32 ? 1 : 0; p.alpha = a->alpha; p.eps = a->eps;
-    return cuda_status(sharq::launch_residual_norm(p, static_cast<cudaStream_t>(stream)));
+    return cuda_status(sharq::launch_residual_norm(p, static_cast<cudaStream_t>(stream), sharq::device_sm_count()));
 }
 
 sharq_status sharq_prepare_int8(const void* X_bf16, const void* gamma_bf16, float eps,

@@ -124,16 +124,6 @@ struct Geometry {
     uint32_t tmem_cols;
 };
 
-// Bounded wait.  mbar_wait() reads the global timer as soon as a first try
-// fails, and that read takes longer than a k-step; a try suspends the thread
-// by itself, so a few hundred of them come first.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
-#pragma unroll 1
-    for (int i = 0; i < 256; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity);
-}
-
 __device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __device__ __forceinline__ int ld_shared_cluster_s32(const int* p, uint32_t rank) {

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "common.cuh"
+
 namespace sharq {
 
 constexpr unsigned kFull = 0xffffffffu;
@@ -68,6 +70,16 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
     return v;
+}
+
+// Bounded wait.  mbar_wait() reads the global timer as soon as a first try
+// fails, and that read takes longer than a k-step; a try suspends the thread
+// by itself, so a few hundred of them come first.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity);
 }
 
 // Sum (or maximum) over the block, returned to every thread.  `red` holds

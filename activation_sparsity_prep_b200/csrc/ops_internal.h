@@ -30,7 +30,7 @@ struct NormLaunch {
     int x_fp32, h_fp32, norm_fp32, mod_fp32;
     float alpha, eps;
 };
-cudaError_t launch_residual_norm(const NormLaunch& p, cudaStream_t s);
+cudaError_t launch_residual_norm(const NormLaunch& p, cudaStream_t s, int sms);
 
 struct RouteLaunch {
     const void* logits;
@@ -82,7 +82,8 @@ struct Int8Launch {
 };
 cudaError_t launch_linear_int8(const Int8Launch& p, cudaStream_t s, int sms);
 
-// Reads and clears int8.cu's device status word.
+// Read and clear the device status words of these files.
+unsigned take_status_norm();
 unsigned take_status_int8();
 
 }  // namespace sharq

@@ -750,38 +750,61 @@ cudaError_t launch_route_n(const RouteLaunch& given, const DispatchLaunch* order
 
 // ----------------------------------------------------------- combine ------
 // out[t] = residual[t] + sum_j weights[t, j] * Y[position[t, j]], fp32, j
-// ascending, the residual last, one rounding.  One block a token and 2048
-// columns; a thread owns 8 columns and issues the loads of up to 8 experts'
-// rows together: bound by memory.
-template <bool YF32, bool OF32>
+// ascending, the residual last, one rounding.  A thread owns 8 columns of one
+// token and issues the loads of J experts' rows before it uses the first:
+// bound by memory.
+__device__ __forceinline__ void widen(const uint4& w, float (&v)[8]) {
+    v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+    v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+}
+__device__ __forceinline__ void widen(const float4 (&w)[2], float (&v)[8]) {
+    v[0] = w[0].x; v[1] = w[0].y; v[2] = w[0].z; v[3] = w[0].w;
+    v[4] = w[1].x; v[5] = w[1].y; v[6] = w[1].z; v[7] = w[1].w;
+}
+
+template <bool F32> struct Raw8 { uint4 w; };
+template <> struct Raw8<true> { float4 w[2]; };
+
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_raw(const void* p, int64_t at) {
+    Raw8<F32> r;
+    if constexpr (F32) {
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+        r.w[0] = __ldg(q);
+        r.w[1] = __ldg(q + 1);
+    } else {
+        r.w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
+    }
+    return r;
+}
+
+template <bool YF32, bool OF32, int J>
 __global__ void __launch_bounds__(256)
 combine_kernel(const CombineLaunch a) {
     const int64_t t = blockIdx.x;
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
     if (c >= a.N) return;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int j0 = 0; j0 < a.k; j0 += 8) {
-        float v[8][8], w[8];
+    const int32_t* position = a.position + t * a.k;
+    const float* weights = a.weights + t * a.k;
+    for (int j0 = 0; j0 < a.k; j0 += J) {
+        Raw8<YF32> v[J];
+        bool in[J];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            w[j] = 0.0f;
-            int64_t at = -1;
-            if (j0 + j < a.k) {
-                at = a.position[t * a.k + j0 + j];
-                w[j] = a.weights[t * a.k + j0 + j];
-            }
-            const bool ok = at >= 0 && at < a.rows;
-            if (ok) load8<YF32>(a.Y, at * a.N + c, v[j]);
-            else {
-                w[j] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-            }
+        for (int j = 0; j < J; ++j) {
+            const int64_t at = j0 + j < a.k ? position[j0 + j] : -1;
+            in[j] = at >= 0 && at < a.rows;
+            if (in[j]) v[j] = load_raw<YF32>(a.Y, at * a.N + c);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < J; ++j) {
+            if (!in[j]) continue;                        // uniform over the block
+            const float w = weights[j0 + j];
+            float x[8];
+            widen(v[j].w, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], v[j][i], sum[i]);
+            for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, x[i], sum[i]);
+        }
     }
     if (a.residual) {
         float r[8];
@@ -790,6 +813,17 @@ combine_kernel(const CombineLaunch a) {
         for (int i = 0; i < 8; ++i) sum[i] += r[i];
     }
     store8<OF32>(a.out, t * a.N + c, sum);
+}
+
+template <bool YF32, bool OF32>
+cudaError_t launch_combine_t(const CombineLaunch& p, cudaStream_t s) {
+    const int chunks = p.N / 8;
+    const int threads = chunks < 256 ? (chunks + 31) / 32 * 32 : 256;
+    const dim3 grid((unsigned)p.T, (unsigned)((chunks + threads - 1) / threads));
+    if (p.k <= 2)      combine_kernel<YF32, OF32, 2><<<grid, threads, 0, s>>>(p);
+    else if (p.k <= 4) combine_kernel<YF32, OF32, 4><<<grid, threads, 0, s>>>(p);
+    else               combine_kernel<YF32, OF32, 8><<<grid, threads, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -815,17 +849,8 @@ cudaError_t launch_dispatch(const DispatchLaunch& p, cudaStream_t s) {
 
 cudaError_t launch_combine(const CombineLaunch& p, cudaStream_t s) {
     if (p.T == 0) return cudaSuccess;
-    const int chunks = p.N / 8;
-    const int threads = chunks < 256 ? (chunks + 31) / 32 * 32 : 256;
-    const dim3 grid((unsigned)p.T, (unsigned)((chunks + threads - 1) / threads));
-    if (p.y_fp32) {
-        if (p.out_fp32) combine_kernel<true, true><<<grid, threads, 0, s>>>(p);
-        else            combine_kernel<true, false><<<grid, threads, 0, s>>>(p);
-    } else {
-        if (p.out_fp32) combine_kernel<false, true><<<grid, threads, 0, s>>>(p);
-        else            combine_kernel<false, false><<<grid, threads, 0, s>>>(p);
-    }
-    return cudaGetLastError();
+    if (p.y_fp32) return p.out_fp32 ? launch_combine_t<true, true>(p, s) : launch_combine_t<true, false>(p, s);
+    return p.out_fp32 ? launch_combine_t<false, true>(p, s) : launch_combine_t<false, false>(p, s);
 }
 
 }  // namespace sharq
