@@ -21,7 +21,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-    "-shared", "--expt-relaxed-constexpr",
+    "-shared", "--expt-relaxed-constexpr", "--threads", "0",
 ]
 
 

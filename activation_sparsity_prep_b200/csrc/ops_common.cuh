@@ -21,6 +21,68 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+// Two fp32 values in one register pair: sm_100 adds, multiplies and fuses both
+// in one instruction.
+using f2 = unsigned long long;
+
+__device__ __forceinline__ f2 make_f2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split_f2(f2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 bf16x2_f2(uint32_t w) { return make_f2(bf16_lo(w), bf16_hi(w)); }
+
+// Eight consecutive elements as four pairs, and back.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, int64_t at, f2 (&v)[4]) {
+    if constexpr (F32) {
+        const ulonglong2* q = reinterpret_cast<const ulonglong2*>(static_cast<const float*>(p) + at);
+        const ulonglong2 a = q[0], b = q[1];
+        v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+    } else {
+        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
+        v[0] = bf16x2_f2(w.x); v[1] = bf16x2_f2(w.y); v[2] = bf16x2_f2(w.z); v[3] = bf16x2_f2(w.w);
+    }
+}
+__device__ __forceinline__ void load8(const void* p, int f32, int64_t at, f2 (&v)[4]) {
+    if (f32) load8<true>(p, at, v);
+    else     load8<false>(p, at, v);
+}
+__device__ __forceinline__ uint32_t pack_f2(f2 v) {
+    float lo, hi;
+    split_f2(v, lo, hi);
+    return pack_bf16(lo, hi);
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, int64_t at, const f2 (&v)[4]) {
+    if constexpr (F32) {
+        ulonglong2* q = reinterpret_cast<ulonglong2*>(static_cast<float*>(p) + at);
+        q[0] = make_ulonglong2(v[0], v[1]);
+        q[1] = make_ulonglong2(v[2], v[3]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) =
+            make_uint4(pack_f2(v[0]), pack_f2(v[1]), pack_f2(v[2]), pack_f2(v[3]));
+    }
+}
+
 // Eight consecutive elements at element offset `at` (16-byte aligned).
 template <bool F32>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
@@ -34,11 +96,6 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) 
         v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
         v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
     }
-}
-
-__device__ __forceinline__ void load8(const void* p, int f32, int64_t at, float (&v)[8]) {
-    if (f32) load8<true>(p, at, v);
-    else     load8<false>(p, at, v);
 }
 
 // One rounding (nearest even) per element where the destination is bf16.
