@@ -45,7 +45,7 @@ sharq_status quantize_rows(const void* X, const void* gamma, float eps, int8_t* 
         return SHARQ_ERR_INVALID_ARG;
     if ((M > 0 && !X) || !aligned(X, 16) || !aligned(gamma, 16)) return SHARQ_ERR_INVALID_ARG;
     sharq::NormLaunch p{};
-    p.x = X; p.ldx = K; p.M = M; p.K = K; p.group_rows = M;
+    p.x = X; p.ldx = K; p.M = M; p.K = K; p.group_rows = M; p.alpha = 1.0f;
     p.gamma = gamma; p.norm = gamma ? SHARQ_NORM_RMS : SHARQ_NORM_NONE; p.eps = eps;
     p.codes = codes; p.row_scale = scales;
     return cuda_status(sharq::launch_residual_norm(p, static_cast<cudaStream_t>(stream), sharq::device_sm_count()));

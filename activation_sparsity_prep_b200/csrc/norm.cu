@@ -87,17 +87,17 @@ __device__ __forceinline__ void vectors_ab(const NormLaunch& a, int64_t group, i
     }
 }
 
-// Starts the copies of a row's x and h into a stage.
-__device__ __forceinline__ void fetch(const NormLaunch& a, int64_t row, uint8_t* stage, uint64_t* bar) {
+// Starts the copies of a row's x and, at h_at, h into a stage.
+__device__ __forceinline__ void fetch(const NormLaunch& a, int64_t row, uint8_t* stage, uint32_t h_at, uint64_t* bar) {
     mbar_arrive_expect_tx(bar, row_bytes(a));
     bulk_load(stage, static_cast<const uint8_t*>(a.x) + row * a.ldx * (a.x_fp32 ? 4 : 2), x_bytes(a), bar);
     if (a.h)
-        bulk_load(stage + x_bytes(a), static_cast<const uint8_t*>(a.h) + row * a.ldh * (a.h_fp32 ? 4 : 2),
+        bulk_load(stage + h_at, static_cast<const uint8_t*>(a.h) + row * a.ldh * (a.h_fp32 ? 4 : 2),
                   row_bytes(a) - x_bytes(a), bar);
 }
 
-// The row's 8-bit codes and scale.  WHOLE: no chunk lies past the row.
-template <int V, bool WHOLE>
+// The row's 8-bit codes and scale.
+template <int V>
 __device__ __forceinline__ void write_codes(const NormLaunch& a, int64_t row, const f2 (&t)[V][4], float (&red)[2][32],
                                             int& turn) {
     float m = 0.0f;
@@ -118,7 +118,7 @@ __device__ __forceinline__ void write_codes(const NormLaunch& a, int64_t row, co
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = i * blockDim.x + threadIdx.x;
-        if (WHOLE || c < a.K >> 3)
+        if (c < a.K >> 3)
             *reinterpret_cast<uint2*>(out + c * 8) =
                 make_uint2(quantize4(t[i][0], t[i][1], inv), quantize4(t[i][2], t[i][3], inv));
     }
@@ -150,7 +150,7 @@ residual_norm_kernel(const __grid_constant__ NormLaunch a, int stages) {
             fence_barrier_init();
             for (int s = 0; s < stages; ++s)
                 if (blockIdx.x + s * (int64_t)gridDim.x < a.M)
-                    fetch(a, blockIdx.x + s * (int64_t)gridDim.x, ring + s * row_size, &full[s]);
+                    fetch(a, blockIdx.x + s * (int64_t)gridDim.x, ring + s * row_size, x_bytes(a), &full[s]);
         }
         __syncthreads();
     }
@@ -248,7 +248,7 @@ residual_norm_kernel(const __grid_constant__ NormLaunch a, int stages) {
         if (RING) {
             __syncthreads();                              // the stage is read: its next row may come
             const int64_t next = row + stages * (int64_t)gridDim.x;
-            if (tid == 0 && next < a.M) fetch(a, next, ring + s * row_size, &full[s]);
+            if (tid == 0 && next < a.M) fetch(a, next, ring + s * row_size, x_bytes(a), &full[s]);
         }
         if (a.out_x) {
             uint8_t* out = static_cast<uint8_t*>(a.out_x) + row * a.ldo * (XF32 ? 4 : 2);
@@ -325,19 +325,19 @@ residual_norm_kernel(const __grid_constant__ NormLaunch a, int stages) {
             for (int i = 0; i < V; ++i)
                 if (i * width + tid < chunks) store8<false>(out, (i * width + tid) * 8, t[i]);
         }
-        if (a.codes) write_codes<V, false>(a, row, t, red, turn);
+        if (a.codes) write_codes<V>(a, row, t, red, turn);
         if (!RING) return;
         if (++s == stages) { s = 0; phase ^= 1; }
     }
 }
 
 // The usual row: every vector has one bf16 source (P = post_gamma or gate,
-// A = gamma or 1 + scale, B = beta or shift), alpha is 1, h is bf16 and the
-// row is whole chunks of the block.  The ring form with the vectors held raw
-// in registers, no bounds checks, and the norms fixed at compile time: the
-// general form issues 480 instructions a warp and row at V = 2, most of them
-// on flags and addresses, and leaves room for fewer blocks.  The arithmetic is
-// that of the general form.
+// A = gamma or 1 + scale, B = beta or shift), alpha is 1 and h is bf16.  The
+// ring form with the vectors held raw in registers and the norms fixed at
+// compile time: the general form issues 480 instructions a warp and row at
+// V = 2, most of them on flags and addresses, and leaves room for fewer
+// blocks.  A stage is padded with zeros to whole chunks of the block, so that
+// only stores look at the row's end.  The arithmetic is the general form's.
 template <int V, bool XF32, int NORM, int H>      // H: 0 no h, 1 added, 2 normed and added
 __global__ void __launch_bounds__(512, V <= 2 ? 2 : 1)
 residual_norm_fast_kernel(const __grid_constant__ NormLaunch a, int stages) {
@@ -347,14 +347,22 @@ residual_norm_fast_kernel(const __grid_constant__ NormLaunch a, int stages) {
     int turn = 0;
     const int tid = threadIdx.x, width = blockDim.x;
     const float inv_k = 1.0f / (float)a.K;
-    const uint32_t row_size = row_bytes(a);
+    const int chunks = a.K >> 3;
+    const bool last = (V - 1) * width + tid < chunks;     // of a thread's chunks only the last can lie past the row
+    const uint32_t pitch_x = V * width * 8 * (XF32 ? 4 : 2), pitch = pitch_x + (H ? V * width * 16 : 0);
     if (tid == 0) {
         for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
         fence_barrier_init();
         for (int s = 0; s < stages; ++s)
             if (blockIdx.x + s * (int64_t)gridDim.x < a.M)
-                fetch(a, blockIdx.x + s * (int64_t)gridDim.x, ring + s * row_size, &full[s]);
+                fetch(a, blockIdx.x + s * (int64_t)gridDim.x, ring + s * pitch, pitch_x, &full[s]);
     }
+    if (!last)
+        for (int s = 0; s < stages; ++s) {
+            const f2 zero[4] = {0, 0, 0, 0};
+            store8<XF32>(ring + s * pitch, ((V - 1) * width + tid) * 8, zero);
+            if (H) store8<false>(ring + s * pitch + pitch_x, ((V - 1) * width + tid) * 8, zero);
+        }
     __syncthreads();
     const bool has_p = H && (a.post_gamma || a.gate), has_a = NORM && (a.gamma || a.scale);
     const bool has_b = NORM && (a.beta || a.shift), plus_one = a.scale != nullptr;
@@ -373,6 +381,8 @@ residual_norm_fast_kernel(const __grid_constant__ NormLaunch a, int stages) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int at = i * width + tid;
+                vp[i] = va[i] = vb[i] = make_uint4(0, 0, 0, 0);
+                if (i == V - 1 && !last) continue;
                 if (has_p) vp[i] = reinterpret_cast<const uint4*>(p)[at];
                 if (has_a) va[i] = reinterpret_cast<const uint4*>(m)[at];
                 if (has_b) vb[i] = reinterpret_cast<const uint4*>(c)[at];
@@ -380,15 +390,15 @@ residual_norm_fast_kernel(const __grid_constant__ NormLaunch a, int stages) {
         }
         wait_bar(&full[s], phase);                        // a wait that gives up is recorded; the row is then wrong
         f2 t[V][4], u[V][4];
-        const uint8_t* stage = ring + s * row_size;
+        const uint8_t* stage = ring + s * pitch;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             load8<XF32>(stage, (i * width + tid) * 8, t[i]);
-            if (H) load8<false>(stage + x_bytes(a), (i * width + tid) * 8, u[i]);
+            if (H) load8<false>(stage + pitch_x, (i * width + tid) * 8, u[i]);
         }
         __syncthreads();                                  // the stage is read: its next row may come
         const int64_t next = row + stages * (int64_t)gridDim.x;
-        if (tid == 0 && next < a.M) fetch(a, next, ring + s * row_size, &full[s]);
+        if (tid == 0 && next < a.M) fetch(a, next, ring + s * pitch, pitch_x, &full[s]);
         float lo, hi;
         if (H == 2) {
             f2 ss = 0;
@@ -422,7 +432,8 @@ residual_norm_fast_kernel(const __grid_constant__ NormLaunch a, int stages) {
         if (a.out_x) {
             uint8_t* out = static_cast<uint8_t*>(a.out_x) + row * a.ldo * (XF32 ? 4 : 2);
 #pragma unroll
-            for (int i = 0; i < V; ++i) store8<XF32>(out, (i * width + tid) * 8, t[i]);
+            for (int i = 0; i < V; ++i)
+                if (i < V - 1 || last) store8<XF32>(out, (i * width + tid) * 8, t[i]);
         }
         if (NORM) {
             if (NORM == 2) {
@@ -436,8 +447,9 @@ residual_norm_fast_kernel(const __grid_constant__ NormLaunch a, int stages) {
                 const f2 minus = make_f2(-mean, -mean);
 #pragma unroll
                 for (int i = 0; i < V; ++i)
+                    if (i < V - 1 || last)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) t[i][j] = add2(t[i][j], minus);
+                        for (int j = 0; j < 4; ++j) t[i][j] = add2(t[i][j], minus);
             }
             f2 ss = 0;
 #pragma unroll
@@ -476,9 +488,10 @@ residual_norm_fast_kernel(const __grid_constant__ NormLaunch a, int stages) {
         if (a.y) {
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.y) + row * a.K;
 #pragma unroll
-            for (int i = 0; i < V; ++i) store8<false>(out, (i * width + tid) * 8, t[i]);
+            for (int i = 0; i < V; ++i)
+                if (i < V - 1 || last) store8<false>(out, (i * width + tid) * 8, t[i]);
         }
-        if (a.codes) write_codes<V, true>(a, row, t, red, turn);
+        if (a.codes) write_codes<V>(a, row, t, red, turn);
         if (++s == stages) { s = 0; phase ^= 1; }
     }
 }
@@ -493,12 +506,57 @@ cudaError_t ring_limit_once(std::atomic<bool> (&done)[64], Fn kernel) {
     return e;
 }
 
+// Blocks of `threads` threads that an SM's registers hold.
+template <class Fn>
+int by_registers(std::atomic<int>& regs, Fn kernel, int threads) {
+    int r = regs.load(std::memory_order_relaxed);
+    if (!r) {
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, kernel) != cudaSuccess) return 1;
+        regs.store(r = (at.numRegs + 7) / 8 * 8, std::memory_order_relaxed);
+    }
+    return std::max(1, 65536 / (r * threads));
+}
+
+// Returns cudaErrorNotSupported where a row does not fit the ring twice or the
+// modulation changes before a block has used it a few times.
 template <int V, bool XF32, int NORM, int H>
-cudaError_t launch_fast(const NormLaunch& p, int grid, int threads, int stages, cudaStream_t s) {
+cudaError_t launch_fast(const NormLaunch& p, int threads, cudaStream_t s, int sms) {
+    const auto kernel = residual_norm_fast_kernel<V, XF32, NORM, H>;
+    static std::atomic<int> regs;
+    // as many blocks an SM as its registers hold and as leave each two rows
+    const int pitch = V * threads * 8 * ((XF32 ? 4 : 2) + (H ? 2 : 0));
+    int resident = std::min({32, 2048 / threads, by_registers(regs, kernel, threads)});
+    while (resident > 1 && kRingBytes / resident - 1024 < 2 * pitch) --resident;
+    const int stages = std::min(kMaxRing, (kRingBytes / resident - 1024) / pitch);
+    if (stages < 2 || ((p.gate || p.scale || p.shift) && p.group_rows < (int64_t)2 * resident * sms))
+        return cudaErrorNotSupported;
     static std::atomic<bool> done[64];
-    if (cudaError_t e = ring_limit_once(done, residual_norm_fast_kernel<V, XF32, NORM, H>); e != cudaSuccess) return e;
-    residual_norm_fast_kernel<V, XF32, NORM, H><<<(unsigned)grid, threads, stages * row_bytes(p), s>>>(p, stages);
+    if (cudaError_t e = ring_limit_once(done, kernel); e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)std::min<int64_t>(p.M, (int64_t)resident * sms);
+    kernel<<<grid, threads, stages * pitch, s>>>(p, stages);
     return cudaGetLastError();
+}
+
+template <int V, bool XF32>
+cudaError_t launch_fast_any(const NormLaunch& p, int threads, cudaStream_t s, int sms) {
+    const int h = !p.h ? 0 : p.post_gamma ? 2 : 1;
+    if constexpr (V > 4) {
+        // longer rows: registers for the plain quantiser only
+        return p.norm || h ? cudaErrorNotSupported : launch_fast<V, XF32, 0, 0>(p, threads, s, sms);
+    } else {
+        switch (p.norm * 3 + h) {
+            case 0: return launch_fast<V, XF32, 0, 0>(p, threads, s, sms);
+            case 1: return launch_fast<V, XF32, 0, 1>(p, threads, s, sms);
+            case 2: return launch_fast<V, XF32, 0, 2>(p, threads, s, sms);
+            case 3: return launch_fast<V, XF32, 1, 0>(p, threads, s, sms);
+            case 4: return launch_fast<V, XF32, 1, 1>(p, threads, s, sms);
+            case 5: return launch_fast<V, XF32, 1, 2>(p, threads, s, sms);
+            case 6: return launch_fast<V, XF32, 2, 0>(p, threads, s, sms);
+            case 7: return launch_fast<V, XF32, 2, 1>(p, threads, s, sms);
+            default: return launch_fast<V, XF32, 2, 2>(p, threads, s, sms);
+        }
+    }
 }
 
 template <int V, bool XF32>
@@ -508,27 +566,11 @@ cudaError_t launch_v(const NormLaunch& p, cudaStream_t s, int sms) {
     const int row = (int)row_bytes(p);
     const bool mod = p.gate || p.scale || p.shift;
     const bool few = p.M <= (int64_t)most * sms;          // a block a row: no ring
-    if constexpr (V <= 4) {
-        const bool plain = p.K == V * threads * 8 && p.alpha == 1.0f && !p.h_fp32 && !p.norm_fp32 && !p.mod_fp32 &&
-                           !(p.post_gamma && p.gate) && !(p.gamma && p.scale) && !(p.beta && (p.shift || p.scale));
-        // as many blocks an SM as leave each two rows of the ring
-        int resident = most;
-        while (resident > 1 && kRingBytes / resident - 1024 < 2 * row) --resident;
-        const int stages = std::min(kMaxRing, (kRingBytes / resident - 1024) / row);
-        if (!few && plain && stages >= 2 && (!mod || p.group_rows >= (int64_t)2 * resident * sms)) {
-            const int grid = resident * sms, h = !p.h ? 0 : p.post_gamma ? 2 : 1;
-            switch (p.norm * 3 + h) {
-                case 0: return launch_fast<V, XF32, 0, 0>(p, grid, threads, stages, s);
-                case 1: return launch_fast<V, XF32, 0, 1>(p, grid, threads, stages, s);
-                case 2: return launch_fast<V, XF32, 0, 2>(p, grid, threads, stages, s);
-                case 3: return launch_fast<V, XF32, 1, 0>(p, grid, threads, stages, s);
-                case 4: return launch_fast<V, XF32, 1, 1>(p, grid, threads, stages, s);
-                case 5: return launch_fast<V, XF32, 1, 2>(p, grid, threads, stages, s);
-                case 6: return launch_fast<V, XF32, 2, 0>(p, grid, threads, stages, s);
-                case 7: return launch_fast<V, XF32, 2, 1>(p, grid, threads, stages, s);
-                default: return launch_fast<V, XF32, 2, 2>(p, grid, threads, stages, s);
-            }
-        }
+    const bool plain = p.alpha == 1.0f && !p.h_fp32 && !p.norm_fp32 && !p.mod_fp32 && !(p.post_gamma && p.gate) &&
+                       !(p.gamma && p.scale) && !(p.beta && (p.shift || p.scale));
+    if (!few && plain) {
+        const cudaError_t e = launch_fast_any<V, XF32>(p, threads, s, sms);
+        if (e != cudaErrorNotSupported) return e;
     }
     // the general ring: its vectors lie behind the rows.  Not for few rows,
     // rows too long for it, or modulation that changes before a block has
@@ -559,9 +601,15 @@ unsigned take_status_norm() { return take_tu_status(); }
 
 cudaError_t launch_residual_norm(const NormLaunch& p, cudaStream_t s, int sms) {
     if (p.M == 0) return cudaSuccess;
-    // at most 512 threads; the split of a row depends on K alone
-    if (p.K <= 2048) return launch_x<1>(p, s, sms);
-    if (p.K <= 8192) return launch_x<2>(p, s, sms);
+    // At most 512 threads; the split of a row depends on K and on the parts of
+    // the call, not on M.  Four chunks a thread halve what a row's reductions
+    // and flags cost a warp, and pay where that counts: the bf16 quantiser and
+    // two norms (4096 x 3584: 11.7 -> 8.4 us, 22.6 -> 20.5 us); with one
+    // reduction and more bytes two chunks keep more warps resident (8190 x
+    // 5120 fp32: 84 against 94 us).
+    const bool long_work = p.K > 3200 && !p.x_fp32 && (!p.h || p.post_gamma);
+    if (p.K <= 256) return launch_x<1>(p, s, sms);
+    if (p.K <= 8192 && !long_work) return launch_x<2>(p, s, sms);
     if (p.K <= 16384) return launch_x<4>(p, s, sms);
     return launch_x<8>(p, s, sms);
 }
