@@ -109,16 +109,61 @@ __device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t adesc, uint6
                  :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
+// The same over a pair of blocks: each holds 128 rows of A and D and half of
+// B's rows at the same shared-memory offsets; the even block issues.
+__device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// Arrives on the barrier at this offset in both blocks of the pair once all
+// prior tcgen05 operations of this thread finish.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+
+// Cluster address of `p` in the even block of the pair.
+__device__ __forceinline__ uint32_t even_addr(const void* p) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+
+// TMA load into this block's shared memory that completes on the even block's
+// barrier.  One block reads each tile: no multicast.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, uint64_t* bar, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4}], [%2];"
+                 :: "r"(smem_u32(dst)), "l"(tmap), "r"(even_addr(bar)), "r"(x), "r"(y) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_even(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(even_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(dst_smem)), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(ncols) : "memory");
+}
+
 // Instruction descriptor: s32 accumulator (2 at bit 4), signed 8-bit A and B
 // (1 at bits 7 and 10), N >> 3 at bit 17, M >> 4 at bit 24.
-__host__ __device__ constexpr uint32_t i8_idesc(int n) {
-    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+__host__ __device__ constexpr uint32_t i8_idesc(int n, int m = kRows) {
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 struct Geometry {
     int bn;                  // rows of the N-side operand of a tile
     int stages;
     int mt, nt;              // tiles along the M-side and the N-side operand
+    int bn2, nt2;            // tiled form: narrower tiles behind the nt of width bn, or none
     int n_fast;              // tile walk: N-side fastest
     int split;               // swapped form: blocks of a cluster that share a tile's K
     uint32_t tmem_cols;
@@ -148,16 +193,25 @@ struct Ring {
     }
 };
 
-// Issues the TMA loads of k-steps [k0, k1) of one tile.
+// Issues the TMA loads of k-steps [k0, k1) of one tile.  PAIR: both blocks'
+// loads complete on the even block's barrier, which expects the bytes of both.
+template <bool PAIR>
 __device__ __forceinline__ bool produce(const CUtensorMap* ta, const CUtensorMap* tb, I8Barriers* bars, uint8_t* smem,
-                                        uint32_t stride, int stages, Ring& at, int k0, int k1, int arow, int brow) {
+                                        uint32_t stride, uint32_t bytes, int stages, Ring& at, int k0, int k1, int arow, int brow,
+                                        bool lead = true) {
     for (int k = k0; k < k1; ++k, at.next(stages)) {
         if (!__all_sync(kFull, wait_bar(&bars->empty[at.s], at.phase ^ 1))) return false;
         uint8_t* st = smem + at.s * stride;
         if (elect_one()) {
-            mbar_arrive_expect_tx(&bars->full[at.s], stride);
-            tma_load_2d(st, ta, &bars->full[at.s], k * kStep, arow);
-            tma_load_2d(st + kABytes, tb, &bars->full[at.s], k * kStep, brow);
+            if constexpr (PAIR) {
+                if (lead) mbar_arrive_expect_tx(&bars->full[at.s], 2 * bytes);
+                tma_load_2d_pair(st, ta, &bars->full[at.s], k * kStep, arow);
+                tma_load_2d_pair(st + kABytes, tb, &bars->full[at.s], k * kStep, brow);
+            } else {
+                mbar_arrive_expect_tx(&bars->full[at.s], bytes);
+                tma_load_2d(st, ta, &bars->full[at.s], k * kStep, arow);
+                tma_load_2d(st + kABytes, tb, &bars->full[at.s], k * kStep, brow);
+            }
         }
         __syncwarp();
     }
@@ -174,6 +228,7 @@ __device__ __forceinline__ void drain(I8Barriers* bars, int stages, Ring at, boo
 }
 
 // Multiplies nk staged k-steps into the accumulator at tensor-memory address d.
+template <bool PAIR>
 __device__ __forceinline__ bool multiply(I8Barriers* bars, uint64_t desc0, uint32_t stride, int stages, Ring& at,
                                          int nk, uint32_t d, uint32_t idesc) {
     for (int k = 0; k < nk; ++k, at.next(stages)) {
@@ -182,15 +237,19 @@ __device__ __forceinline__ bool multiply(I8Barriers* bars, uint64_t desc0, uint3
         const uint64_t da = desc0 + at.s * (stride >> 4), db = da + (kABytes >> 4);
         if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < kStep / 32; ++j)
-                tc_mma_i8(d, da + 2 * j, db + 2 * j, idesc, (k | j) ? 1u : 0u);
-            tc_commit(&bars->empty[at.s]);
+            for (int j = 0; j < kStep / 32; ++j) {
+                if constexpr (PAIR) tc_mma_i8_pair(d, da + 2 * j, db + 2 * j, idesc, (k | j) ? 1u : 0u);
+                else                tc_mma_i8(d, da + 2 * j, db + 2 * j, idesc, (k | j) ? 1u : 0u);
+            }
+            if constexpr (PAIR) tc_commit_pair(&bars->empty[at.s]);
+            else                tc_commit(&bars->empty[at.s]);
         }
         __syncwarp();
     }
     return true;
 }
 
+template <bool PAIR>
 __device__ __forceinline__ uint8_t* setup(uint8_t* raw, const Geometry& g, uint32_t stride, I8Barriers*& bars,
                                           uint8_t*& tail) {
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -204,66 +263,90 @@ __device__ __forceinline__ uint8_t* setup(uint8_t* raw, const Geometry& g, uint3
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 4);
+            mbar_init(&bars->acc_empty[b], PAIR ? 8 : 4);
         }
         fence_barrier_init();
     }
-    if (threadIdx.x >> 5 == 1) { tmem_alloc(&bars->tmem_base, g.tmem_cols); tmem_relinquish(); }
+    if (threadIdx.x >> 5 == 1) {
+        if constexpr (PAIR) tmem_alloc_pair(&bars->tmem_base, g.tmem_cols);
+        else { tmem_alloc(&bars->tmem_base, g.tmem_cols); tmem_relinquish(); }
+    }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync_all();                         // the other block's barriers are ready too
     tc_fence_after();
     return smem;
 }
 
-__device__ __forceinline__ void tile_at(const Geometry& g, int t, int& m, int& n) {
-    if (g.n_fast) { m = t / g.nt; n = t - m * g.nt; }
+// Tile t of the tiled form: its row tile, first column and width.
+struct Tile { int m, col, width; };
+__device__ __forceinline__ Tile tile_at(const Geometry& g, int t) {
+    const int full = g.mt * g.nt;
+    const bool wide = t < full;
+    const int nt = wide ? g.nt : g.nt2, bn = wide ? g.bn : g.bn2;
+    if (!wide) t -= full;
+    int m, n;
+    if (g.n_fast) { m = t / nt; n = t - m * nt; }
     else          { n = t / g.mt; m = t - n * g.mt; }
+    return {m, (wide ? 0 : g.nt * g.bn) + n * bn, bn};
 }
 
 // Tiled form.  A = tokens, B = channels; two accumulators of bn columns, so
-// the next tile's MMAs run while the epilogue drains the previous one.  A
+// the next tile's MMAs run while the epilogue drains the previous one.  PAIR:
+// a tile is 256 tokens over two blocks of a cluster, each loading its 128
+// tokens and half of the channels: a third less traffic from L2 for a tile as
+// wide (single blocks of 256 columns ask for 19 TB/s and wait for it).  A
 // thread drains one token's columns, 128 bytes of output at a time, through
 // a staging buffer that turns them into whole 128-byte row segments.
-template <bool YF32>
+template <bool YF32, bool PAIR>
 __global__ void __launch_bounds__(kI8Threads, 1)
-tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const Int8Launch a,
-             const Geometry g) {
+tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+             const __grid_constant__ CUtensorMap tb2, const Int8Launch a, const Geometry g) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t stride = kABytes + g.bn * kStep;
+    constexpr int kShare = PAIR ? 2 : 1;                  // blocks that share a tile's channels
+    const uint32_t stride = kABytes + g.bn / kShare * kStep;
     I8Barriers* bars;
     uint8_t* tail;
-    uint8_t* smem = setup(smem_raw, g, stride, bars, tail);
+    uint8_t* smem = setup<PAIR>(smem_raw, g, stride, bars, tail);
     const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t tmem = __shfl_sync(kFull, bars->tmem_base, 0);
     const int nk = (a.K + kStep - 1) / kStep;
-    const int tiles = g.mt * g.nt;
+    const int tiles = g.mt * (g.nt + g.nt2);
+    const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;     // place in the pair
+    const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
+    constexpr int kTileRows = kShare * kRows;
 
     if (warp == 0) {
         if (elect_one()) { prefetch_tmap(&ta); prefetch_tmap(&tb); }
         __syncwarp();
         Ring at{0, 0};
         int done = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, done = 1) {
-            int m, n;
-            tile_at(g, t, m, n);
-            if (!produce(&ta, &tb, bars, smem, stride, g.stages, at, 0, nk, m * kRows, n * g.bn)) {
-                drain(bars, g.stages, at, done || at.phase);
+        for (int t = first; t < tiles; t += step, done = 1) {
+            const Tile w = tile_at(g, t);
+            const int brows = w.width / kShare;           // channels that this block loads
+            if (!produce<PAIR>(&ta, w.width == g.bn ? &tb : &tb2, bars, smem, stride, kABytes + brows * kStep, g.stages,
+                               at, 0, nk, w.m * kTileRows + rank * kRows, w.col + rank * brows, rank == 0)) {
+                if (rank == 0) drain(bars, g.stages, at, done || at.phase);
                 break;
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         Ring at{0, 0};
         const uint64_t desc0 = sdesc_sw128(smem_u32(smem));
         uint32_t tc = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++tc) {
+        for (int t = first; t < tiles; t += step, ++tc) {
             const uint32_t buf = tc & 1, use = tc >> 1;
             if (use > 0 && !__all_sync(kFull, wait_bar(&bars->acc_empty[buf], (use - 1) & 1))) break;
             tc_fence_after();
-            if (!multiply(bars, desc0, stride, g.stages, at, nk, tmem + buf * g.bn, i8_idesc(g.bn))) break;
-            if (elect_one()) tc_commit(&bars->acc_full[buf]);
+            if (!multiply<PAIR>(bars, desc0, stride, g.stages, at, nk, tmem + buf * g.bn, i8_idesc(tile_at(g, t).width, kTileRows)))
+                break;
+            if (elect_one()) {
+                if constexpr (PAIR) tc_commit_pair(&bars->acc_full[buf]);
+                else                tc_commit(&bars->acc_full[buf]);
+            }
             __syncwarp();
         }
-    } else {
+    } else if (warp >= 2) {
         constexpr int kCols = YF32 ? 32 : 64;             // columns of one staged 128-byte row segment
         const int q = warp & 3;
         const uint32_t lane_off = (uint32_t)(q * 32) << 16;
@@ -274,12 +357,11 @@ tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUt
         const bool vec = (int64_t)a.N % (YF32 ? 4 : 8) == 0;
         uint32_t tc = 0;
         bool ok = true;                                   // after a wait that gave up: keep step, store nothing
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++tc) {
-            int m, n;
-            tile_at(g, t, m, n);
-            const int64_t row0 = (int64_t)m * kRows + q * 32, col0 = (int64_t)n * g.bn;
+        for (int t = first; t < tiles; t += step, ++tc) {
+            const Tile w = tile_at(g, t);
+            const int64_t row0 = (int64_t)w.m * kTileRows + rank * kRows + q * 32, col0 = w.col;
             epilogue_bar();                               // the previous tile's columns are no longer read
-            for (int c = et; c < g.bn; c += 128) {
+            for (int c = et; c < w.width; c += 128) {
                 const bool in = col0 + c < a.N;
                 col_scale[c] = in ? a.w_scale[col0 + c] : 0.0f;
                 col_bias[c] = in ? bias_at(a, col0 + c) : 0.0f;
@@ -290,29 +372,32 @@ tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUt
             ok = __all_sync(kFull, ok && wait_bar(&bars->acc_full[buf], use & 1));
             tc_fence_after();
             if (!ok) continue;
-            for (int c0 = 0; c0 < g.bn; c0 += kCols) {
+            for (int c0 = 0; c0 < w.width; c0 += kCols) {
                 uint32_t v[kCols];
 #pragma unroll
                 for (int h = 0; h < kCols; h += 32)
                     tmem_ld_32x32b_x32(tmem + buf * g.bn + lane_off + c0 + h, *reinterpret_cast<uint32_t(*)[32]>(v + h));
                 tmem_ld_wait();
-                if (c0 + kCols >= g.bn) {
+                if (c0 + kCols >= w.width) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->acc_empty[buf]);
+                    if (lane == 0) {
+                        if constexpr (PAIR) mbar_arrive_even(&bars->acc_empty[buf]);
+                        else                mbar_arrive(&bars->acc_empty[buf]);
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {             // 16-byte units of the row segment
                     uint4 o;
-                    uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+                    uint32_t* word = reinterpret_cast<uint32_t*>(&o);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if constexpr (YF32) {
                             const int c = u * 4 + i;
-                            w[i] = __float_as_uint(finish((int)v[c], xs, col_scale[c0 + c], col_bias[c0 + c]));
+                            word[i] = __float_as_uint(finish((int)v[c], xs, col_scale[c0 + c], col_bias[c0 + c]));
                         } else {
                             const int c = u * 8 + i * 2;
-                            w[i] = pack_bf16(finish((int)v[c], xs, col_scale[c0 + c], col_bias[c0 + c]),
+                            word[i] = pack_bf16(finish((int)v[c], xs, col_scale[c0 + c], col_bias[c0 + c]),
                                              finish((int)v[c + 1], xs, col_scale[c0 + c + 1], col_bias[c0 + c + 1]));
                         }
                     }
@@ -349,7 +434,12 @@ tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUt
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) { tc_fence_after(); tmem_dealloc(tmem, g.tmem_cols); }
+    if (PAIR) cluster_sync_all();                         // neither block leaves while the other may signal it
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, g.tmem_cols);
+        else                tmem_dealloc(tmem, g.tmem_cols);
+    }
 }
 
 // Swapped form.  A = 128 channels, B = all M <= bn tokens; the `split` blocks
@@ -363,7 +453,7 @@ swapped_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     const uint32_t stride = kABytes + g.bn * kStep;
     I8Barriers* bars;
     uint8_t* tail;
-    uint8_t* smem = setup(smem_raw, g, stride, bars, tail);
+    uint8_t* smem = setup<false>(smem_raw, g, stride, bars, tail);
     const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t tmem = __shfl_sync(kFull, bars->tmem_base, 0);
     const int nk = (a.K + kStep - 1) / kStep;
@@ -375,11 +465,11 @@ swapped_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
         if (elect_one()) { prefetch_tmap(&tw); prefetch_tmap(&tx); }
         __syncwarp();
         Ring at{0, 0};
-        if (!produce(&tw, &tx, bars, smem, stride, g.stages, at, k0, k1, tile * kRows, 0))
+        if (!produce<false>(&tw, &tx, bars, smem, stride, stride, g.stages, at, k0, k1, tile * kRows, 0))
             drain(bars, g.stages, at, at.phase);
     } else if (warp == 1) {
         Ring at{0, 0};
-        if (multiply(bars, sdesc_sw128(smem_u32(smem)), stride, g.stages, at, k1 - k0, tmem, i8_idesc(g.bn)) && elect_one())
+        if (multiply<false>(bars, sdesc_sw128(smem_u32(smem)), stride, g.stages, at, k1 - k0, tmem, i8_idesc(g.bn)) && elect_one())
             tc_commit(&bars->acc_full[0]);
     }
     __syncwarp();
@@ -476,40 +566,92 @@ uint32_t tmem_cols(int n) {
     return c;
 }
 
-template <bool YF32>
-cudaError_t launch_tiled_t(const CUtensorMap& ta, const CUtensorMap& tb, const Int8Launch& p, const Geometry& g,
-                           size_t smem, int grid, cudaStream_t s) {
+template <bool YF32, bool PAIR>
+cudaError_t launch_tiled_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tb2, const Int8Launch& p,
+                           const Geometry& g, size_t smem, int grid, cudaStream_t s) {
     static std::atomic<bool> done[64];
-    if (cudaError_t e = smem_limit_once(done, tiled_kernel<YF32>); e != cudaSuccess) return e;
-    tiled_kernel<YF32><<<grid, kI8Threads, smem, s>>>(ta, tb, p, g);
-    return cudaGetLastError();
+    if (cudaError_t e = smem_limit_once(done, tiled_kernel<YF32, PAIR>); e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kI8Threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, tiled_kernel<YF32, PAIR>, ta, tb, tb2, p, g);
+}
+
+// Time of a tile of this width a k-step, in units of 1.3 ns, measured over 128
+// k-steps: pairs of blocks 156, 176, 237, 313 ns for 64 to 256 channels,
+// single blocks (half as many rows) 148, 220, 297, 396 ns.
+int64_t tile_cost(bool pair, int bn) { return pair ? std::max(121, 30 + bn * 83 / 100) : bn + 47; }
+
+// Shape and order of the tiles.  All of one width, or 256 wide for as many
+// whole waves as there are and narrower behind, so that a last wave of a few
+// tiles does not take a whole tile's time (4096 x 3584: 224 pair tiles are
+// 3.03 waves).
+bool plan_tiles(const Int8Launch& p, int sms, Geometry& g) {
+    int64_t best = 0;
+    bool pair = false;
+    for (int two = 1; two >= 0; --two) {
+        const int rows = two ? 2 * kRows : kRows, units = two ? sms / 2 : sms;
+        const int64_t mt = (p.M + rows - 1) / rows;
+        auto take = [&](int bn, int64_t nt, int bn2, int64_t nt2) {
+            // the unit with most work is the first, or the first without one more wide tile
+            const int64_t wide = mt * nt, all = wide + mt * nt2;
+            int64_t cost = 0;
+            for (const int64_t c : {(int64_t)0, wide % units}) {
+                const int64_t n1 = (wide - c + units - 1) / units, n = (all - c + units - 1) / units;
+                cost = std::max(cost, n1 * tile_cost(two, bn) + (n - n1) * tile_cost(two, bn2));
+            }
+            if (best && cost >= best) return;
+            best = cost;
+            pair = two;
+            g.bn = bn; g.nt = (int)nt; g.bn2 = bn2; g.nt2 = (int)nt2; g.mt = (int)mt;
+        };
+        for (int bn = 256; bn >= 64; bn -= 64) take(bn, (p.N + bn - 1) / bn, 64, 0);
+        const int64_t waves = mt * ((p.N + 255) / 256) / units;
+        for (int64_t w = std::max<int64_t>(1, waves - 1); w <= waves; ++w) {
+            const int64_t nt = std::min<int64_t>(w * units / mt, p.N / 256);
+            const int64_t rest = p.N - nt * 256;
+            if (nt > 0 && rest > 0)
+                for (int bn = 192; bn >= 64; bn -= 64) take(256, nt, bn, (rest + bn - 1) / bn);
+        }
+    }
+    return pair;
 }
 
 cudaError_t launch_tiled(const Int8Launch& p, cudaStream_t s, int sms) {
     Geometry g{};
-    g.mt = (int)((p.M + kRows - 1) / kRows);
-    // tile width: the one whose waves over the SMs take least MMA time; a
-    // narrow tile re-reads the tokens more often and is charged for 32 more
-    // columns than it has
-    int64_t best = 0;
-    for (int bn = 256; bn >= 64; bn -= 64) {
-        const int64_t tiles = (int64_t)g.mt * ((p.N + bn - 1) / bn);
-        const int64_t cost = (tiles + sms - 1) / sms * (bn + 32);
-        if (!best || cost < best) { best = cost; g.bn = bn; }
-    }
-    g.nt = (p.N + g.bn - 1) / g.bn;
+    sms = std::max(2, sms);
+    const bool pair = plan_tiles(p, sms, g);
     g.n_fast = p.M > p.N;                                 // the smaller operand stays in L2
     g.split = 1;
     g.tmem_cols = tmem_cols(2 * g.bn);
-    const uint32_t stride = kABytes + g.bn * kStep;
+    const int share = pair ? 2 : 1;
+    const uint32_t stride = kABytes + g.bn / share * kStep;
     g.stages = std::min<int>(kMaxStages, (int)((227 * 1024 - 1024 - kBarBytes - kEpilogueBytes) / stride));
     const size_t smem = 1024 + g.stages * stride + kBarBytes + kEpilogueBytes;
-    CUtensorMap ta, tb;
-    if (!make_map(&ta, p.x, p.M, p.K, kRows) || !make_map(&tb, p.w, p.N, p.K, g.bn)) return cudaErrorInvalidValue;
-    const int64_t tiles = (int64_t)g.mt * g.nt;
-    if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
-    const int grid = (int)std::min<int64_t>(tiles, std::max(1, sms));
-    return p.y_fp32 ? launch_tiled_t<true>(ta, tb, p, g, smem, grid, s) : launch_tiled_t<false>(ta, tb, p, g, smem, grid, s);
+    CUtensorMap ta, tb, tb2;
+    if (!make_map(&ta, p.x, p.M, p.K, kRows) || !make_map(&tb, p.w, p.N, p.K, g.bn / share)) return cudaErrorInvalidValue;
+    if (g.nt2) {
+        if (!make_map(&tb2, p.w, p.N, p.K, g.bn2 / share)) return cudaErrorInvalidValue;
+    } else {
+        tb2 = tb;
+    }
+    const int64_t tiles = (int64_t)g.mt * (g.nt + g.nt2);
+    if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
+    const int grid = share * (int)std::min<int64_t>(tiles, sms / share);
+    if (pair)
+        return p.y_fp32 ? launch_tiled_t<true, true>(ta, tb, tb2, p, g, smem, grid, s)
+                        : launch_tiled_t<false, true>(ta, tb, tb2, p, g, smem, grid, s);
+    return p.y_fp32 ? launch_tiled_t<true, false>(ta, tb, tb2, p, g, smem, grid, s)
+                    : launch_tiled_t<false, false>(ta, tb, tb2, p, g, smem, grid, s);
 }
 
 cudaError_t launch_swapped(const Int8Launch& p, cudaStream_t s, int sms) {
