@@ -91,6 +91,8 @@ constexpr int kRows = 128;                    // rows of the M-side operand of a
 constexpr int kStep = 128;                    // K a pipeline stage: one 128-byte swizzled row
 constexpr uint32_t kABytes = kRows * kStep;
 constexpr int kMaxStages = 8;
+constexpr int kMaxSplit = 8;                  // blocks of a cluster that share a tile's K
+constexpr int kSwappedTokens = 64;            // most tokens of the swapped form
 constexpr int kI8Threads = 192;               // TMA warp, MMA warp, four epilogue warps
 
 struct alignas(8) I8Barriers {
@@ -170,10 +172,6 @@ struct Geometry {
 };
 
 __device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-__device__ __forceinline__ int ld_shared_cluster_s32(const int* p, uint32_t rank) {
-    return __float_as_int(ld_shared_cluster_f32(p, rank));
-}
 
 // One lane of a converged warp.  The TMA and MMA warps run their loops with
 // all lanes and elect one around the instructions: loop state and descriptors
@@ -445,7 +443,17 @@ tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUt
 // Swapped form.  A = 128 channels, B = all M <= bn tokens; the `split` blocks
 // of a cluster take a run of k-steps each, leave their int32 partial tiles in
 // shared memory, and every block then adds up and finishes its share of the
-// tokens over distributed shared memory (integer sums: exact in any order).
+// tokens over distributed shared memory (integer sums: exact in any order),
+// a warp a token, four channels a lane, the ranks' loads in flight together.
+__device__ __forceinline__ int4 ld_shared_cluster_v4(const int* p, uint32_t rank) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
 __global__ void __launch_bounds__(kI8Threads)
 swapped_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const Int8Launch a,
                const Geometry g) {
@@ -460,6 +468,8 @@ swapped_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     const int tile = blockIdx.x / g.split, rank = blockIdx.x - tile * g.split;
     const int k0 = (int)((int64_t)nk * rank / g.split), k1 = (int)((int64_t)nk * (rank + 1) / g.split);
     int* partial = reinterpret_cast<int*>(smem);          // [tokens][128], over the stages once they are consumed
+    float* xs = reinterpret_cast<float*>(tail);           // [kSwappedTokens] token scales
+    const int M = (int)a.M;
 
     if (warp == 0) {
         if (elect_one()) { prefetch_tmap(&tw); prefetch_tmap(&tx); }
@@ -473,38 +483,65 @@ swapped_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
             tc_commit(&bars->acc_full[0]);
     }
     __syncwarp();
-    const int q = warp & 3;
-    const int jl = q * 32 + lane;
-    const int64_t j = (int64_t)tile * kRows + jl;
-    float ws = 0.0f, bias = 0.0f;
-    const int M = (int)a.M;
     if (warp >= 2) {
-        if (j < a.N) { ws = a.w_scale[j]; bias = bias_at(a, j); }
-        const bool ok = wait_bar(&bars->acc_full[0], 0);
+        const int q = warp & 3;
+        const int jl = q * 32 + lane;
+        const int64_t j = (int64_t)tile * kRows + jl;
+        for (int i = threadIdx.x - 64; i < M; i += 128) xs[i] = a.x_scale[i];
+        const float ws = j < a.N ? a.w_scale[j] : 0.0f, bias = j < a.N ? bias_at(a, j) : 0.0f;
+        epilogue_bar();
+        const bool ok = __all_sync(kFull, wait_bar(&bars->acc_full[0], 0));
         tc_fence_after();
-        if (__all_sync(kFull, ok)) {
+        if (ok) {
             for (int c0 = 0; c0 < M; c0 += 16) {
                 uint32_t v[16];
                 tmem_ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
                 tmem_ld_wait();
+                if (g.split > 1) {
+                    // bn tokens of room: those past M are written and not read
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (c0 + i >= M) break;
-                    if (g.split > 1) partial[(c0 + i) * kRows + jl] = (int)v[i];
-                    else if (j < a.N) store_one(a, c0 + i, j, finish((int)v[i], a.x_scale[c0 + i], ws, bias));
+                    for (int i = 0; i < 16; ++i) partial[(c0 + i) * kRows + jl] = (int)v[i];
+                } else if (j < a.N) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c0 + i < M) store_one(a, c0 + i, j, finish((int)v[i], xs[c0 + i], ws, bias));
                 }
             }
         }
+        __syncwarp();
     }
-    __syncwarp();
     if (g.split > 1) {
         cluster_sync_all();
-        if (warp >= 2 && j < a.N) {
-            const int t0 = M * rank / g.split, t1 = M * (rank + 1) / g.split;
-            for (int i = t0; i < t1; ++i) {
-                int sum = 0;
-                for (int r = 0; r < g.split; ++r) sum += ld_shared_cluster_s32(&partial[i * kRows + jl], r);
-                store_one(a, i, j, finish(sum, a.x_scale[i], ws, bias));
+        const int t0 = M * rank / g.split, t1 = M * (rank + 1) / g.split;
+        const int64_t j = (int64_t)tile * kRows + lane * 4;
+        if (t0 + warp < t1 && j < a.N) {
+            float ws[4], bias[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                ws[c] = j + c < a.N ? a.w_scale[j + c] : 0.0f;
+                bias[c] = j + c < a.N ? bias_at(a, j + c) : 0.0f;
+            }
+            for (int i = t0 + warp; i < t1; i += kI8Threads / 32) {
+                int4 v[kMaxSplit];
+#pragma unroll
+                for (int r = 0; r < kMaxSplit; ++r)
+                    if (r < g.split) v[r] = ld_shared_cluster_v4(&partial[i * kRows + lane * 4], r);
+                int4 sum = v[0];
+#pragma unroll
+                for (int r = 1; r < kMaxSplit; ++r)
+                    if (r < g.split) { sum.x += v[r].x; sum.y += v[r].y; sum.z += v[r].z; sum.w += v[r].w; }
+                const float y[4] = {finish(sum.x, xs[i], ws[0], bias[0]), finish(sum.y, xs[i], ws[1], bias[1]),
+                                    finish(sum.z, xs[i], ws[2], bias[2]), finish(sum.w, xs[i], ws[3], bias[3])};
+                const int64_t to = (int64_t)i * a.N + j;
+                if (a.N % 4 == 0) {
+                    if (a.y_fp32) *reinterpret_cast<float4*>(static_cast<float*>(a.Y) + to) = make_float4(y[0], y[1], y[2], y[3]);
+                    else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.Y) + to) =
+                             make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (j + c < a.N) store_one(a, i, j + c, y[c]);
+                }
             }
         }
         __syncwarp();
@@ -663,16 +700,14 @@ cudaError_t launch_swapped(const Int8Launch& p, cudaStream_t s, int sms) {
     const int nk = (p.K + kStep - 1) / kStep;
     // fewer tiles than SMs: split K so that a cluster of blocks shares a
     // tile, each keeping at least 4 k-steps
-    g.split = std::max(1, std::min({8, nk / 4, std::max(1, sms) / g.mt}));
+    g.split = std::max(1, std::min({kMaxSplit, nk / 4, std::max(1, sms) / g.mt}));
     const uint32_t stride = kABytes + g.bn * kStep;
-    // two blocks an SM where their stages fit: one loads while the other finishes
-    const uint32_t room = (g.bn <= 64 ? 112 : 226) * 1024 - 1024 - kBarBytes;
+    // two blocks an SM: one loads while the other finishes
+    constexpr uint32_t kExtra = kBarBytes + kSwappedTokens * 4;
+    const uint32_t room = 112 * 1024 - 1024 - kExtra;
     g.stages = std::min<int>({kMaxStages, (int)(room / stride), std::max(2, (nk + g.split - 1) / g.split)});
-    uint32_t need = g.stages * stride;
-    if (g.split > 1) need = std::max<uint32_t>(need, (uint32_t)p.M * kRows * 4);
-    // the partial tiles lie over the stages: keep the barriers behind both
-    while (g.stages * stride < need) ++g.stages;
-    const size_t smem = 1024 + g.stages * stride + kBarBytes;
+    // the partial tiles, bn x 512 bytes, lie over the stages (bn <= 64: two hold 36 KB or more)
+    const size_t smem = 1024 + g.stages * stride + kExtra;
     CUtensorMap tw, tx;
     if (!make_map(&tw, p.w, p.N, p.K, kRows) || !make_map(&tx, p.x, p.M, p.K, g.bn)) return cudaErrorInvalidValue;
     static std::atomic<bool> done[64];
@@ -699,9 +734,7 @@ unsigned take_status_int8() { return take_tu_status(); }
 cudaError_t launch_linear_int8(const Int8Launch& p, cudaStream_t s, int sms) {
     if (p.M == 0) return cudaSuccess;
     if (p.M == 1) return launch_dot<1>(p, s);
-    if (p.M <= 4) return launch_dot<4>(p, s);
-    if (p.M <= 8) return launch_dot<8>(p, s);
-    if (p.M <= 256) return launch_swapped(p, s, sms);
+    if (p.M <= kSwappedTokens) return launch_swapped(p, s, sms);
     return launch_tiled(p, s, sms);
 }
 
