@@ -7,13 +7,13 @@
 // finish(), so a row's result does not depend on the batch around it.
 //
 // Three forms:
-//   dot     few tokens: a warp a channel on the dot-product units, bound by
-//           streaming the weight;
-//   swapped up to 256 tokens: 128 channels x all tokens on the tensor cores
+//   dot     one or two tokens: a warp for two channels on the dot-product
+//           units, bound by streaming the weight;
+//   swapped up to 64 tokens: 128 channels x all tokens on the tensor cores
 //           (the weight is the M-side operand), K split over a cluster so
 //           that narrow layers use every SM; bound by the weight;
-//   tiled   128 tokens x up to 256 channels a tile, persistent, bound by the
-//           tensor cores.
+//   tiled   128 or 256 tokens x up to 256 channels a tile, persistent, bound
+//           by the tensor cores.
 #include <cuda.h>
 
 #include <algorithm>
@@ -57,6 +57,7 @@ dot_kernel(const Int8Launch a) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) x[m] = reinterpret_cast<const int4*>(a.x + min((int64_t)m, a.M - 1) * a.K);
     int acc[MT][R] = {};
+#pragma unroll 4
     for (int c = lane; c < a.K / 16; c += 32) {
         int4 wv[R];
 #pragma unroll
@@ -81,7 +82,7 @@ dot_kernel(const Int8Launch a) {
 
 template <int MT>
 cudaError_t launch_dot(const Int8Launch& p, cudaStream_t s) {
-    constexpr int R = 4;
+    constexpr int R = 2;
     dot_kernel<MT, R><<<(unsigned)((p.N + 8 * R - 1) / (8 * R)), 256, 0, s>>>(p);
     return cudaGetLastError();
 }
@@ -733,8 +734,16 @@ unsigned take_status_int8() { return take_tu_status(); }
 
 cudaError_t launch_linear_int8(const Int8Launch& p, cudaStream_t s, int sms) {
     if (p.M == 0) return cudaSuccess;
-    if (p.M == 1) return launch_dot<1>(p, s);
-    if (p.M <= kSwappedTokens) return launch_swapped(p, s, sms);
+    // One or two tokens: the dot form starts sooner (4096 x 4096: 3.4 and 3.8
+    // us against 5.7), but its warps walk long rows alone (4096 x 14336: 15.3
+    // against 13.5 us), and at two tokens it streams at 4.9 TB/s against 6
+    // (28672 x 4096: 24.1 against 21.6 us).
+    const int64_t bytes = (int64_t)p.N * p.K;
+    if (p.K <= 8192 && (p.M == 1 || (p.M == 2 && bytes <= (64 << 20))))
+        return p.M == 1 ? launch_dot<1>(p, s) : launch_dot<2>(p, s);
+    // Up to 64 tokens, unless K is short: nothing to split, and the tiled form
+    // has less to set up (48 x 1024 x 1024: 4.5 against 5.9 us).
+    if (p.M <= kSwappedTokens && p.K > 1024) return launch_swapped(p, s, sms);
     return launch_tiled(p, s, sms);
 }
 
