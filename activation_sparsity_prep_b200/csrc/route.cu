@@ -541,6 +541,19 @@ __device__ __forceinline__ void load_batch(const DispatchLaunch& a, int64_t at, 
         if ((unsigned)e[b] >= (unsigned)a.E) e[b] = -1;
 }
 
+// Lanes that hold the same expert (any set for e < 0).  One ballot a bit of
+// the expert: the warp match instruction takes a step for each distinct value,
+// and here nearly all are.
+__device__ __forceinline__ unsigned same_expert(int e, int bits) {
+    unsigned peers = kFull;
+    for (int b = 0; b < bits; ++b) {
+        const bool set = e >> b & 1;
+        const unsigned with = __ballot_sync(kFull, set);
+        peers &= set ? with : ~with;
+    }
+    return peers & __ballot_sync(kFull, e >= 0);
+}
+
 // Exclusive scan of v over the block's 1024 threads; sum: the total.
 __device__ __forceinline__ int block_scan(int v, int* wsum, int& sum) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -577,6 +590,7 @@ __device__ __forceinline__ void dispatch_body(const DispatchLaunch& a, int* smem
     const int64_t first = ((int64_t)rank * kDispWarps + warp) * per;
     const int64_t end = first + per < a.n ? first + per : a.n;
     int* mine = hist + warp * a.E;
+    const int bits = 32 - __clz(a.E - 1);          // 0 for one expert
 
     for (int i = threadIdx.x; i < kDispWarps * a.E; i += blockDim.x) hist[i] = 0;
     __syncthreads();
@@ -625,8 +639,9 @@ __device__ __forceinline__ void dispatch_body(const DispatchLaunch& a, int* smem
         load_batch(a, at, end, lane, e);
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
+            if (at + b * 32 >= end) break;
             const int64_t i = at + b * 32 + lane;
-            const unsigned peers = __match_any_sync(kFull, e[b]);
+            const unsigned peers = same_expert(e[b], bits);
             int slot = -1;
             if (e[b] >= 0) slot = start[e[b]] + mine[e[b]] + __popc(peers & ((1u << lane) - 1u));
             __syncwarp();
