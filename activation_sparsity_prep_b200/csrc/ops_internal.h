@@ -45,6 +45,7 @@ struct RouteLaunch {
     int group_size;
     int group_whole;            // a group is a power-of-two number of whole lanes
     int group_shift;            // log2 of the lanes that share a group
+    int vectors;                // rows can be loaded in vectors
 };
 
 struct DispatchLaunch {

@@ -51,38 +51,44 @@ __device__ __forceinline__ double smaller(double a, double b) { return a < b ? a
 // Lane i of the warp that routes a token holds experts NPL i .. NPL i + NPL-1:
 // a row is loaded in vectors, and a gather in lane order is in expert order.
 // -inf where masked: beyond E, a logit or a bias of -inf or NaN.
-template <int NPL, bool F32, bool VEC>
+template <int NPL, bool F32>
+__device__ __forceinline__ void load_vectors(const RouteLaunch& a, int64_t t, int e0, float (&l)[NPL]) {
+    constexpr int kBytes = NPL * (F32 ? 4 : 2);
+    uint32_t w[(kBytes + 3) / 4];
+    const char* p = static_cast<const char*>(a.logits) + (t * a.ld + e0) * (F32 ? 4 : 2);
+    if constexpr (kBytes >= 16)
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i)
+            *reinterpret_cast<uint4*>(w + 4 * i) = *reinterpret_cast<const uint4*>(p + 16 * i);
+    else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+    else if constexpr (kBytes == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
+    else w[0] = *reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+        const float v = F32 ? __uint_as_float(w[j]) : j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+        l[j] = fmaxf(v, kNegInf);                         // -inf for NaN
+    }
+}
+
+__device__ __forceinline__ float logit_at(const RouteLaunch& a, int64_t at) {
+    return a.fp32 ? static_cast<const float*>(a.logits)[at]
+                  : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at]);
+}
+
+template <int NPL>
 __device__ __forceinline__ void load_logits(const RouteLaunch& a, int64_t t, int lane, float (&l)[NPL]) {
     const int e0 = lane * NPL;
-    if constexpr (VEC) {
-        constexpr int kBytes = NPL * (F32 ? 4 : 2);
-        uint32_t w[(kBytes + 3) / 4];
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) l[j] = kNegInf;
+    if (a.vectors) {                                      // whole lanes, aligned
         if (e0 < a.E) {
-            const char* p = static_cast<const char*>(a.logits) + (t * a.ld + e0) * (F32 ? 4 : 2);
-            if constexpr (kBytes >= 16)
-#pragma unroll
-                for (int i = 0; i < kBytes / 16; ++i)
-                    *reinterpret_cast<uint4*>(w + 4 * i) = *reinterpret_cast<const uint4*>(p + 16 * i);
-            else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
-            else if constexpr (kBytes == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
-            else w[0] = *reinterpret_cast<const uint16_t*>(p);
-        }
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) {
-            const float v = F32 ? __uint_as_float(w[j]) : j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-            l[j] = e0 < a.E ? fmaxf(v, kNegInf) : kNegInf;      // -inf for NaN
+            if (a.fp32) load_vectors<NPL, true>(a, t, e0, l);
+            else        load_vectors<NPL, false>(a, t, e0, l);
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < NPL; ++j) {
-            float v = kNegInf;
-            if (e0 + j < a.E) {
-                const int64_t at = t * a.ld + e0 + j;
-                v = F32 ? static_cast<const float*>(a.logits)[at]
-                        : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at]);
-            }
-            l[j] = fmaxf(v, kNegInf);
-        }
+        for (int j = 0; j < NPL; ++j)
+            if (e0 + j < a.E) l[j] = fmaxf(logit_at(a, t * a.ld + e0 + j), kNegInf);
     }
 }
 
@@ -104,11 +110,11 @@ __device__ __forceinline__ bool load_bias(const RouteLaunch& a, int lane, float 
 // the caller then repeats it in double, so that the experts are those of the
 // formula and not of its rounding.  Without a bias the scores' order is that
 // of the logits, which needs no evaluation.
-template <int NPL, bool F32, typename F>
+template <int NPL, typename F>
 __device__ bool choose(const RouteLaunch& a, int64_t t, int lane, F* scratch) {
     constexpr bool kFp32 = sizeof(F) == 4;
     float l[NPL], b[NPL];
-    load_logits<NPL, F32, false>(a, t, lane, l);
+    load_logits(a, t, lane, l);
     load_bias(a, lane, b);
     F s[NPL], key[NPL];
 #pragma unroll
@@ -325,19 +331,19 @@ enum Choice { kChosen, kTooClose, kTooMany };
 // F = float leaves close decisions to F = double (kTooClose), which gathers
 // on its keys rounded to fp32, an order-preserving step, and ranks the keys
 // themselves.  Nothing is written unless kChosen is returned.
-template <int NPL, bool F32, bool VEC, typename F>
+template <int NPL, bool SCORED, bool GROUPS, typename F>
 __device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, int lane, const float (&b)[NPL],
                                               bool bias_masks, F* scratch, RouteScratch& sh) {
     constexpr bool kFp32 = sizeof(F) == 4;
-    const bool scored = a.bias != nullptr;
-    const bool need_all = scored || (a.groups > 1 && a.group_top2);      // every score, not just the chosen ones'
+    constexpr bool scored = SCORED;                                      // a bias: keys are not the logits
+    const bool need_all = SCORED || (GROUPS && a.group_top2);            // every score, not just the chosen ones'
     const float rel = a.sigmoid ? 4.8e-7f : 1.9e-6f;                     // see choose(); the fast exponential is within both
     F key[NPL];
     F m = 0, r = 1;
     {
         float l[NPL];
-        load_logits<NPL, F32, VEC>(a, t, lane, l);
-        if (bias_masks)
+        load_logits(a, t, lane, l);
+        if (SCORED && bias_masks)
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
                 if (!(b[j] > kNegInf)) l[j] = kNegInf;
@@ -370,10 +376,10 @@ __device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, i
         }
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-            s[j] = key[j] > F(kNegInf) ? s[j] + F(b[j]) : F(kNegInf);    // b is 0 without a bias
+            s[j] = key[j] > F(kNegInf) ? (SCORED ? s[j] + F(b[j]) : s[j]) : F(kNegInf);
             if (scored) key[j] = s[j];
         }
-        if (a.groups > 1 && !keep_groups(s, key, a, lane, true, rel, scratch)) return kTooClose;
+        if (GROUPS && !keep_groups(s, key, a, lane, true, rel, scratch)) return kTooClose;
     } else {
         if (!a.sigmoid && !a.renormalize) {
             F sum = 0;
@@ -382,7 +388,7 @@ __device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, i
             sum = warp_sum(sum);
             r = sum > F(0) ? quotient(F(1), sum) : F(0);
         }
-        if (a.groups > 1) keep_groups(key, key, a, lane, false, rel, scratch);
+        if (GROUPS) keep_groups(key, key, a, lane, false, rel, scratch);
     }
 
     // the bound: one more than k where the gap behind the last choice counts
@@ -438,9 +444,7 @@ __device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, i
     }
     const bool chosen = mine && rank < a.k;
     F x = v;
-    if (scored && mine)
-        x = F32 ? static_cast<const float*>(a.logits)[t * a.ld + e]
-                : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[t * a.ld + e]);
+    if (scored && mine) x = logit_at(a, t * a.ld + e);
     F score;
     if (a.sigmoid) {
         score = quotient(F(1), F(1) + exp_of(-x));
@@ -486,28 +490,27 @@ __device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, i
 
 // What the fp32 form leaves undecided.  Not inlined: its registers (the scores
 // in double) would halve the resident warps of the fp32 form.
-template <int NPL, bool F32>
+template <int NPL, bool SCORED, bool GROUPS>
 __device__ __noinline__ void choose_slow(const RouteLaunch* a, int64_t t, int lane, Choice why, double* scratch,
                                          RouteScratch* sh) {
     if (why == kTooClose) {
         float b[NPL];
         const bool masks = load_bias(*a, lane, b);
-        why = choose_fast<NPL, F32, false>(*a, t, lane, b, masks, scratch, *sh);
+        why = choose_fast<NPL, SCORED, GROUPS>(*a, t, lane, b, masks, scratch, *sh);
     }
-    if (why == kTooMany && !choose<NPL, F32>(*a, t, lane, reinterpret_cast<float*>(scratch)))
-        choose<NPL, F32>(*a, t, lane, scratch);
+    if (why == kTooMany && !choose<NPL>(*a, t, lane, reinterpret_cast<float*>(scratch))) choose<NPL>(*a, t, lane, scratch);
 }
 
 // One warp routes token t.  scratch: E doubles of this warp.
-template <int NPL, bool F32, bool VEC>
+template <int NPL, bool SCORED, bool GROUPS>
 __device__ __forceinline__ void route_token(const RouteLaunch& a, int64_t t, int lane, const float (&b)[NPL],
                                             bool bias_masks, double* scratch, RouteScratch& sh) {
-    const Choice c = choose_fast<NPL, F32, VEC>(a, t, lane, b, bias_masks, reinterpret_cast<float*>(scratch), sh);
-    if (c != kChosen) choose_slow<NPL, F32>(&a, t, lane, c, scratch, &sh);
+    const Choice c = choose_fast<NPL, SCORED, GROUPS>(a, t, lane, b, bias_masks, reinterpret_cast<float*>(scratch), sh);
+    if (c != kChosen) choose_slow<NPL, SCORED, GROUPS>(&a, t, lane, c, scratch, &sh);
 }
 
 // One warp a token, a warp walking several.
-template <int NPL, bool F32, bool VEC>
+template <int NPL, bool SCORED, bool GROUPS>
 __global__ void __launch_bounds__(kRouteWarps * 32, NPL <= 8 ? 4 : 2)
 route_kernel(const __grid_constant__ RouteLaunch a) {
     extern __shared__ double route_smem[];
@@ -516,7 +519,7 @@ route_kernel(const __grid_constant__ RouteLaunch a) {
     float b[NPL];
     const bool masks = load_bias(a, lane, b);
     for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.T; t += (int64_t)gridDim.x * kRouteWarps)
-        route_token<NPL, F32, VEC>(a, t, lane, b, masks, route_smem + warp * a.E, sh[warp]);
+        route_token<NPL, SCORED, GROUPS>(a, t, lane, b, masks, route_smem + warp * a.E, sh[warp]);
 }
 
 // ---------------------------------------------------------- dispatch ------
@@ -679,7 +682,7 @@ invert_kernel(const DispatchLaunch a) {
 // Few tokens: the choice and the dispatch order by one block, in one launch.
 constexpr int kFusedTokens = 64;
 
-template <int NPL, bool F32, bool VEC>
+template <int NPL, bool SCORED, bool GROUPS>
 __global__ void __launch_bounds__(kDispWarps * 32)
 route_dispatch_kernel(const __grid_constant__ RouteLaunch r, const DispatchLaunch d) {
     extern __shared__ double route_smem[];
@@ -689,7 +692,7 @@ route_dispatch_kernel(const __grid_constant__ RouteLaunch r, const DispatchLaunc
     float b[NPL];
     const bool masks = load_bias(r, lane, b);
     for (int64_t t = warp; t < r.T; t += kDispWarps)
-        route_token<NPL, F32, VEC>(r, t, lane, b, masks, route_smem + warp * r.E, sh[warp]);
+        route_token<NPL, SCORED, GROUPS>(r, t, lane, b, masks, route_smem + warp * r.E, sh[warp]);
     __syncthreads();                              // the block's own ids, written to global memory, are read back
     dispatch_body<1>(d, reinterpret_cast<int*>(route_smem), wsum);
 }
@@ -728,22 +731,22 @@ cudaError_t launch_dispatch_c(const DispatchLaunch& p, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, dispatch_kernel<C>, p);
 }
 
-template <int NPL, bool F32, bool VEC>
+template <int NPL, bool SCORED, bool GROUPS>
 cudaError_t launch_route_v(const RouteLaunch& p, const DispatchLaunch* order, cudaStream_t s, int sms) {
     if (order && p.T <= kFusedTokens) {
         // scratch of 32 warps and, later, the histograms
         const size_t smem = std::max((size_t)kDispWarps * p.E * sizeof(double), dispatch_smem(p.E));
         static std::atomic<bool> done[64];
-        if (cudaError_t e = allow_smem(done, route_dispatch_kernel<NPL, F32, VEC>,
+        if (cudaError_t e = allow_smem(done, route_dispatch_kernel<NPL, SCORED, GROUPS>,
                                        (size_t)kDispWarps * kMaxRouteExperts * sizeof(double));
             e != cudaSuccess)
             return e;
-        route_dispatch_kernel<NPL, F32, VEC><<<1, kDispWarps * 32, smem, s>>>(p, *order);
+        route_dispatch_kernel<NPL, SCORED, GROUPS><<<1, kDispWarps * 32, smem, s>>>(p, *order);
         return cudaGetLastError();
     }
     const int64_t blocks = std::min<int64_t>((p.T + kRouteWarps - 1) / kRouteWarps, (int64_t)sms * 12);
     const size_t smem = p.groups > 1 ? (size_t)kRouteWarps * p.E * sizeof(double) : 0;
-    route_kernel<NPL, F32, VEC><<<(unsigned)blocks, kRouteWarps * 32, smem, s>>>(p);
+    route_kernel<NPL, SCORED, GROUPS><<<(unsigned)blocks, kRouteWarps * 32, smem, s>>>(p);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     return order ? launch_dispatch(*order, s) : cudaSuccess;
 }
@@ -758,9 +761,9 @@ cudaError_t launch_route_n(const RouteLaunch& given, const DispatchLaunch* order
     while ((2 << p.group_shift) <= most) ++p.group_shift;
     // whole lanes of experts, every lane's first on a boundary of its vector
     const int size = p.fp32 ? 4 : 2, align = std::min(16, NPL * size);
-    const bool vec = p.E % NPL == 0 && p.ld * size % align == 0 && reinterpret_cast<uintptr_t>(p.logits) % align == 0;
-    if (p.fp32) return vec ? launch_route_v<NPL, true, true>(p, order, s, sms) : launch_route_v<NPL, true, false>(p, order, s, sms);
-    return vec ? launch_route_v<NPL, false, true>(p, order, s, sms) : launch_route_v<NPL, false, false>(p, order, s, sms);
+    p.vectors = p.E % NPL == 0 && p.ld * size % align == 0 && reinterpret_cast<uintptr_t>(p.logits) % align == 0;
+    if (p.bias) return p.groups > 1 ? launch_route_v<NPL, true, true>(p, order, s, sms) : launch_route_v<NPL, true, false>(p, order, s, sms);
+    return p.groups > 1 ? launch_route_v<NPL, false, true>(p, order, s, sms) : launch_route_v<NPL, false, false>(p, order, s, sms);
 }
 
 // ----------------------------------------------------------- combine ------
