@@ -241,7 +241,9 @@ SHARQ_API sharq_status sharq_prepare_amax(const void* X_bf16, const float* amax,
  * weight when offsets[e] <= t < offsets[e+1]:
  *   Y[t,j] = G_w[e] * (G_b * S_b[t,j] + G_r * S_r[t,j]).
  * expert_offsets is a DEVICE int32 array [E+1], offsets[0] = 0, offsets[E]
- * = T, non-decreasing; row_index is a DEVICE int32 array [T] of rows < x->M.
+ * <= T, non-decreasing; row_index is a DEVICE int32 array [T] of rows < x->M.
+ * Rows from offsets[E] on (dropped choices, see sharq_moe_dispatch) belong to
+ * no expert: their row_index entries are read, their rows of Y not written.
  * w holds E stacked weights (see sharq_weight), 1 <= E <= 256.  The
  * activation tensor scales are those of the whole prepare call.  Y is [T, N]
  * in dispatch order.  The call first gathers each expert's rows into ws
@@ -380,7 +382,8 @@ SHARQ_API sharq_status sharq_moe_route(const void* logits, int64_t ld, int logit
  * sharq_moe_combine take.  An id outside 0 .. E-1 is dropped: its position
  * is -1 and it takes no row, so offsets[E] counts the live rows; row_index
  * entries from there on are 0, and the grouped linears leave those rows of
- * their output as they were.  1 <= E <= 512, T * k < 2^31. */
+ * their output as they were (zero them where a prepare follows: its tensor
+ * scales span all rows).  1 <= E <= 512, T * k < 2^31. */
 SHARQ_API sharq_status sharq_moe_dispatch(const sharq_routing* r, void* stream);
 
 /* Expert outputs back to the tokens:
