@@ -11,6 +11,7 @@
 namespace {
 
 constexpr int64_t kMaxInt = 2147483647;
+constexpr int64_t kMaxRows8 = (int64_t)1 << 30;     // rows of an 8-bit operand: tile starts stay in int32
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -95,7 +96,7 @@ sharq_status sharq_moe_route(const void* logits, int64_t ld, int logits_fp32, co
 sharq_status sharq_moe_combine(const void* Y, int y_is_fp32, int64_t rows, int N, const int32_t* position,
                                const float* weights, int64_t T, int k, const void* residual, void* out,
                                int out_is_fp32, void* stream) {
-    if (T < 0 || T > kMaxInt || rows < 0 || k < 1 || N < 8 || N % 8 != 0) return SHARQ_ERR_INVALID_ARG;
+    if (T < 0 || T > kMaxInt || rows < 0 || k < 1 || N < 8 || N % 8 != 0 || N > (1 << 24)) return SHARQ_ERR_INVALID_ARG;
     if (T > 0 && (!position || !weights || !out)) return SHARQ_ERR_INVALID_ARG;
     if (rows > 0 && !Y) return SHARQ_ERR_INVALID_ARG;
     if (!aligned(Y, 16) || !aligned(residual, 16) || !aligned(out, 16) || !aligned(position, 4) ||
@@ -148,7 +149,7 @@ sharq_status sharq_quantize_weight_int8(const void* W_bf16, const sharq_weight_i
 
 sharq_status sharq_linear_int8(const sharq_prepared_int8* x, const sharq_weight_int8* w, const void* bias,
                                int bias_is_fp32, void* Y, int y_is_fp32, void* stream) {
-    if (!x || !w || x->M < 0 || x->M > kMaxInt || w->N < 1 || x->K != w->K || w->K < 16 || w->K > 65536 ||
+    if (!x || !w || x->M < 0 || x->M > kMaxRows8 || w->N < 1 || w->N > kMaxRows8 || x->K != w->K || w->K < 16 || w->K > 65536 ||
         w->K % 16 != 0)
         return SHARQ_ERR_INVALID_ARG;
     if (!valid_rows8(x->codes, x->scales, x->M) || !valid_rows8(w->codes, w->scales, w->N))

@@ -858,11 +858,42 @@ cudaError_t launch_route(const RouteLaunch& p, const DispatchLaunch* order, cuda
     return launch_route_n<16>(p, order, s, sms);
 }
 
+namespace {
+// Whether the device places a cluster of 16 blocks of the dispatch kernel at
+// its largest (16 is beyond the portable size).
+bool wide_cluster_fits() {
+    static std::atomic<int> known[64];                    // 0 not asked, 1 no, 2 yes
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64)
+        if (const int k = known[dev].load(std::memory_order_relaxed)) return k == 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kDispWarps * 32);
+    cfg.dynamicSmemBytes = dispatch_smem(kMaxRouteExperts);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool fits = cudaFuncSetAttribute(dispatch_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)cfg.dynamicSmemBytes) == cudaSuccess &&
+                      cudaFuncSetAttribute(dispatch_kernel<16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                      cudaOccupancyMaxActiveClusters(&n, dispatch_kernel<16>, &cfg) == cudaSuccess && n > 0;
+    if (!fits) cudaGetLastError();
+    if (dev < 64) known[dev].store(fits ? 2 : 1, std::memory_order_relaxed);
+    return fits;
+}
+}  // namespace
+
 cudaError_t launch_dispatch(const DispatchLaunch& p, cudaStream_t s) {
     // one block covers up to 4 choices a thread; beyond that a cluster does,
     // of 16 blocks where the device places one
     if (p.n <= 4096) return launch_dispatch_c<1>(p, s);
-    cudaError_t e = p.n > 8 * 4096 ? launch_dispatch_c<16>(p, s) : launch_dispatch_c<8>(p, s);
+    cudaError_t e = p.n > 8 * 4096 && wide_cluster_fits() ? launch_dispatch_c<16>(p, s) : launch_dispatch_c<8>(p, s);
     if (e != cudaSuccess) return e;
     invert_kernel<<<(unsigned)((p.n + 255) / 256), 256, 0, s>>>(p);
     return cudaGetLastError();

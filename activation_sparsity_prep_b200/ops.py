@@ -252,8 +252,8 @@ def moe_combine(Y, position, weights, residual=None, out=None):
     rows, N = Y.shape
     dev = Y.device
     _flat("Y", Y, (rows, N), _BF16_FP32, dev)
-    if N < 8 or N % 8:
-        raise ValueError(f"N={N} must be a multiple of 8")
+    if N < 8 or N % 8 or N > 2 ** 24:
+        raise ValueError(f"N={N} must be a multiple of 8 from 8 to 2^24")
     if not isinstance(position, torch.Tensor) or position.dim() != 2:
         raise ValueError("position must be a 2-D tensor [T, k]")
     T, k = position.shape
@@ -373,8 +373,8 @@ def linear_int8(x: PreparedInt8, w: WeightInt8, bias=None, out_fp32: bool = Fals
         raise ValueError(f"weight K={w.K} does not match the activations' K={x.K}")
     if not 16 <= x.K <= 65536 or x.K % 16:
         raise ValueError(f"K={x.K}, expected a multiple of 16 from 16 to 65536")
-    if w.N < 1:
-        raise ValueError(f"N={w.N}, expected at least 1")
+    if not 1 <= w.N <= 2 ** 30 or x.M > 2 ** 30:
+        raise ValueError(f"M={x.M}, N={w.N}, expected M up to 2^30 and N from 1 to 2^30")
     _check_rows8("x", x, x.M, x.K, dev)
     _check_rows8("weight", w, w.N, w.K, dev)
     if bias is not None:

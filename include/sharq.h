@@ -391,7 +391,8 @@ SHARQ_API sharq_status sharq_moe_dispatch(const sharq_routing* r, void* stream);
  * summed in fp32 with j ascending and the residual last, rounded once.
  * Y [rows, N] bf16 or fp32; residual (or NULL) and out [T, N] bf16 or fp32,
  * alike; out may be the residual itself.  A position outside 0 .. rows-1
- * adds nothing, whatever its weight.  N % 8 == 0, k >= 1, T <= 2^31 - 1. */
+ * adds nothing, whatever its weight.  N % 8 == 0, 8 <= N <= 2^24, k >= 1,
+ * T <= 2^31 - 1. */
 SHARQ_API sharq_status sharq_moe_combine(const void* Y, int y_is_fp32, int64_t rows, int N,
                                          const int32_t* position, const float* weights, int64_t T,
                                          int k, const void* residual, void* out, int out_is_fp32,
@@ -467,8 +468,8 @@ SHARQ_API sharq_status sharq_quantize_weight_int8(const void* W_bf16, const shar
  *   Y[i, j] = (x.scales[i] * sum_k x[i, k] w[j, k]) * w.scales[j] [+ bias[j]],
  * the sum exact in 32-bit integers and rounded once to fp32.  bias [N] fp32
  * (bias_is_fp32) or bf16, or NULL; Y [M, N] bf16 or fp32.  Any codes are
- * allowed, -128 too.  K % 16 == 0, 16 <= K <= 65536, N >= 1, M >= 0; codes
- * and Y 16-byte aligned, scales and bias by their type. */
+ * allowed, -128 too.  K % 16 == 0, 16 <= K <= 65536, 1 <= N <= 2^30, 0 <= M
+ * <= 2^30; codes and Y 16-byte aligned, scales and bias by their type. */
 SHARQ_API sharq_status sharq_linear_int8(const sharq_prepared_int8* x, const sharq_weight_int8* w,
                                          const void* bias, int bias_is_fp32, void* Y, int y_is_fp32,
                                          void* stream);

@@ -2,6 +2,10 @@
 mixture-of-experts block from the residual stream back to it, an attention
 projection in 8 bits, both captured into graphs and on other streams, with
 guarded outputs."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -166,6 +170,35 @@ def test_captured_and_replayed(T):
             assert all(torch.equal(p, q) for p, q in zip(outs, want))
     torch.cuda.synchronize()
     assert sq.last_device_status() == 0
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first call of every operator is captured."""
+    code = """
+import torch, activation_sparsity_prep_b200 as sq
+x = torch.randn(200, 512, device="cuda").bfloat16(); h = x.flip(0).contiguous(); l = torch.randn(5000, 64, device="cuda")
+w = sq.WeightInt8(torch.ones(264, 512, dtype=torch.int8, device="cuda"), torch.ones(264, device="cuda"), 264, 512)
+def run():
+    out = []
+    for n in (1, 50, 200):
+        x2, q = sq.residual_norm(x[:n], h[:n], int8=True)
+        out += [x2, sq.linear_int8(q, w)]
+    for n in (3, 5000):
+        r = sq.moe_route(l[:n], 4, bias=l[0].contiguous(), score="sigmoid")
+        out += [r.ids, r.row_index, sq.moe_combine(x[:n * 4 if n < 50 else 200], r.position, r.weights)]
+    return out
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+assert sq.last_device_status() == 0
+print("captured")
+"""
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert p.returncode == 0 and "captured" in p.stdout, p.stderr[-2000:]
 
 
 def test_other_streams_at_once():

@@ -48,7 +48,7 @@ def test_dispatch_refusals(kw):
     assert lib().sharq_moe_dispatch(None, None) == INVALID
 
 
-@pytest.mark.parametrize("kw", [dict(N=0), dict(N=12), dict(N=-8), dict(rows=-1), dict(T=-1), dict(T=2 ** 31), dict(k=0),
+@pytest.mark.parametrize("kw", [dict(N=0), dict(N=12), dict(N=-8), dict(N=(1 << 24) + 8), dict(rows=-1), dict(T=-1), dict(T=2 ** 31), dict(k=0),
                                 dict(Y=None), dict(position=None), dict(weights=None), dict(out=None), dict(Y=P + 8),
                                 dict(residual=P + 2), dict(out=P + 4), dict(position=P + 2), dict(weights=P + 1)])
 def test_combine_refusals(kw):
@@ -88,7 +88,7 @@ def test_quantise_refusals(kw):
         assert lib().sharq_quantize_weight_int8(f["X"], ctypes.byref(w), None) == INVALID
 
 
-@pytest.mark.parametrize("kw", [dict(M=-1), dict(M=2 ** 31), dict(N=0), dict(K=24), dict(K=0), dict(K=65552), dict(wK=128),
+@pytest.mark.parametrize("kw", [dict(M=-1), dict(M=2 ** 30 + 1), dict(N=2 ** 30 + 1), dict(N=0), dict(K=24), dict(K=0), dict(K=65552), dict(wK=128),
                                 dict(xc=None), dict(xs=None), dict(wc=None), dict(ws=None), dict(Y=None), dict(xc=P + 8),
                                 dict(wc=P + 1), dict(xs=P + 2), dict(ws=P + 1), dict(Y=P + 8), dict(bias=P + 1),
                                 dict(bias=P + 2, bf=1)])
