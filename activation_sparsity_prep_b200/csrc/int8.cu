@@ -7,8 +7,8 @@
 // finish(), so a row's result does not depend on the batch around it.
 //
 // Three forms:
-//   dot     one or two tokens: a warp for two channels on the dot-product
-//           units, bound by streaming the weight;
+//   dot     one or two tokens: a warp for two or four channels on the
+//           dot-product units, bound by streaming the weight;
 //   swapped up to 64 tokens: 128 channels x all tokens on the tensor cores
 //           (the weight is the M-side operand), K split over a cluster so
 //           that narrow layers use every SM; bound by the weight;
@@ -44,11 +44,13 @@ __device__ __forceinline__ void store_one(const Int8Launch& a, int64_t i, int64_
 // ---------------------------------------------------------------- dot -----
 // A warp computes R channels for MT tokens, its lanes striding K in 16-byte
 // pieces.
+constexpr int kDotWarps = 4;
+
 template <int MT, int R>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kDotWarps * 32)
 dot_kernel(const Int8Launch a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int j0 = (blockIdx.x * 8 + warp) * R;
+    const int j0 = (blockIdx.x * kDotWarps + warp) * R;
     if (j0 >= a.N) return;
     const int4* w[R];
     const int4* x[MT];
@@ -57,7 +59,7 @@ dot_kernel(const Int8Launch a) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) x[m] = reinterpret_cast<const int4*>(a.x + min((int64_t)m, a.M - 1) * a.K);
     int acc[MT][R] = {};
-#pragma unroll 4
+#pragma unroll (8 / R)
     for (int c = lane; c < a.K / 16; c += 32) {
         int4 wv[R];
 #pragma unroll
@@ -82,8 +84,11 @@ dot_kernel(const Int8Launch a) {
 
 template <int MT>
 cudaError_t launch_dot(const Int8Launch& p, cudaStream_t s) {
-    constexpr int R = 2;
-    dot_kernel<MT, R><<<(unsigned)((p.N + 8 * R - 1) / (8 * R)), 256, 0, s>>>(p);
+    // two channels a warp where there are few, for more warps; four where there
+    // are many, for fewer loads of the tokens (1 x 14336 x 4096: 11.7 against
+    // 13.6 us; 1 x 4096 x 4096: 3.7 against 3.5 us)
+    if (p.N > 8192) dot_kernel<MT, 4><<<(unsigned)((p.N + 4 * kDotWarps - 1) / (4 * kDotWarps)), kDotWarps * 32, 0, s>>>(p);
+    else            dot_kernel<MT, 2><<<(unsigned)((p.N + 2 * kDotWarps - 1) / (2 * kDotWarps)), kDotWarps * 32, 0, s>>>(p);
     return cudaGetLastError();
 }
 

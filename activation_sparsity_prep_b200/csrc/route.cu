@@ -783,15 +783,17 @@ __device__ __forceinline__ void widen(const float4 (&w)[2], float (&v)[8]) {
 template <bool F32> struct Raw8 { uint4 w; };
 template <> struct Raw8<true> { float4 w[2]; };
 
-template <bool F32>
+// CONST: through the read-only path (memory that the kernel does not write).
+template <bool F32, bool CONST = true>
 __device__ __forceinline__ Raw8<F32> load_raw(const void* p, int64_t at) {
     Raw8<F32> r;
     if constexpr (F32) {
         const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-        r.w[0] = __ldg(q);
-        r.w[1] = __ldg(q + 1);
+        r.w[0] = CONST ? __ldg(q) : q[0];
+        r.w[1] = CONST ? __ldg(q + 1) : q[1];
     } else {
-        r.w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
+        r.w = CONST ? __ldg(q) : *q;
     }
     return r;
 }
@@ -805,6 +807,9 @@ combine_kernel(const CombineLaunch a) {
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const int32_t* position = a.position + t * a.k;
     const float* weights = a.weights + t * a.k;
+    // the residual loads under the experts' rows
+    Raw8<OF32> res;
+    if (a.residual) res = load_raw<OF32, false>(a.residual, t * a.N + c);
     for (int j0 = 0; j0 < a.k; j0 += J) {
         Raw8<YF32> v[J];
         bool in[J];
@@ -826,7 +831,7 @@ combine_kernel(const CombineLaunch a) {
     }
     if (a.residual) {
         float r[8];
-        load8<OF32>(a.residual, t * a.N + c, r);
+        widen(res.w, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] += r[i];
     }
@@ -836,10 +841,10 @@ combine_kernel(const CombineLaunch a) {
 template <bool YF32, bool OF32>
 cudaError_t launch_combine_t(const CombineLaunch& p, cudaStream_t s) {
     const int chunks = p.N / 8;
-    // smaller blocks where a thread holds many rows' loads (4096 x 8 x 2048:
-    // 35.7 us with 128 threads, 37.0 with 256; 8192 x 2 x 5120: 66 against 57)
-    const int most = p.k > 4 ? 128 : 256;
-    const int threads = chunks < most ? (chunks + 31) / 32 * 32 : most;
+    // small blocks: a token's last loads hold back few others (4096 x 8 x 2048:
+    // 31.4 us with 64 threads, 31.9 with 128; 8192 x 2 x 5120: 54.8 against
+    // 58.2 with 256)
+    const int threads = std::min(64, (chunks + 31) / 32 * 32);
     const dim3 grid((unsigned)p.T, (unsigned)((chunks + threads - 1) / threads));
     if (p.k <= 2)      combine_kernel<YF32, OF32, 2><<<grid, threads, 0, s>>>(p);
     else if (p.k <= 4) combine_kernel<YF32, OF32, 4><<<grid, threads, 0, s>>>(p);
