@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kDotWarps * 32)
 dot_kernel(const Int8Launch a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int j0 = (blockIdx.x * kDotWarps + warp) * R;
+    chain_begin();
     if (j0 >= a.N) return;
     const int4* w[R];
     const int4* x[MT];
@@ -87,9 +88,10 @@ cudaError_t launch_dot(const Int8Launch& p, cudaStream_t s) {
     // two channels a warp where there are few, for more warps; four where there
     // are many, for fewer loads of the tokens (1 x 14336 x 4096: 11.7 against
     // 13.6 us; 1 x 4096 x 4096: 3.7 against 3.5 us)
-    if (p.N > 8192) dot_kernel<MT, 4><<<(unsigned)((p.N + 4 * kDotWarps - 1) / (4 * kDotWarps)), kDotWarps * 32, 0, s>>>(p);
-    else            dot_kernel<MT, 2><<<(unsigned)((p.N + 2 * kDotWarps - 1) / (2 * kDotWarps)), kDotWarps * 32, 0, s>>>(p);
-    return cudaGetLastError();
+    const int channels = kDotWarps * (p.N > 8192 ? 4 : 2);
+    const dim3 grid((unsigned)((p.N + channels - 1) / channels));
+    return p.N > 8192 ? launch_chained(dot_kernel<MT, 4>, grid, kDotWarps * 32, 0, s, 1, p)
+                      : launch_chained(dot_kernel<MT, 2>, grid, kDotWarps * 32, 0, s, 1, p);
 }
 
 // ------------------------------------------------------- tensor cores -----
@@ -187,6 +189,11 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+// TMA prefetch of a box into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" :: "l"(tmap), "r"(x), "r"(y) : "memory");
 }
 
 // Place in the ring of stages: the stage's index and the parity of its phase.
@@ -319,6 +326,7 @@ tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUt
     const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;     // place in the pair
     const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
     constexpr int kTileRows = kShare * kRows;
+    chain_begin();
 
     if (warp == 0) {
         if (elect_one()) { prefetch_tmap(&ta); prefetch_tmap(&tb); }
@@ -476,10 +484,17 @@ swapped_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     int* partial = reinterpret_cast<int*>(smem);          // [tokens][128], over the stages once they are consumed
     float* xs = reinterpret_cast<float*>(tail);           // [kSwappedTokens] token scales
     const int M = (int)a.M;
+    if (warp == 0) {
+        // the weight's first stages into L2 before the wait
+        if (elect_one()) {
+            prefetch_tmap(&tw); prefetch_tmap(&tx);
+            for (int k = k0; k < min(k1, k0 + g.stages); ++k) tma_prefetch_2d(&tw, k * kStep, tile * kRows);
+        }
+        __syncwarp();
+    }
+    chain_begin();
 
     if (warp == 0) {
-        if (elect_one()) { prefetch_tmap(&tw); prefetch_tmap(&tx); }
-        __syncwarp();
         Ring at{0, 0};
         if (!produce<false>(&tw, &tx, bars, smem, stride, stride, g.stages, at, k0, k1, tile * kRows, 0))
             drain(bars, g.stages, at, at.phase);
@@ -614,19 +629,7 @@ cudaError_t launch_tiled_t(const CUtensorMap& ta, const CUtensorMap& tb, const C
                            const Geometry& g, size_t smem, int grid, cudaStream_t s) {
     static std::atomic<bool> done[64];
     if (cudaError_t e = smem_limit_once(done, tiled_kernel<YF32, PAIR>); e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kI8Threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, tiled_kernel<YF32, PAIR>, ta, tb, tb2, p, g);
+    return launch_chained(tiled_kernel<YF32, PAIR>, dim3((unsigned)grid), kI8Threads, smem, s, PAIR ? 2 : 1, ta, tb, tb2, p, g);
 }
 
 // Time of a tile of this width a k-step, in units of 1.3 ns, measured over 128
@@ -718,19 +721,7 @@ cudaError_t launch_swapped(const Int8Launch& p, cudaStream_t s, int sms) {
     if (!make_map(&tw, p.w, p.N, p.K, kRows) || !make_map(&tx, p.x, p.M, p.K, g.bn)) return cudaErrorInvalidValue;
     static std::atomic<bool> done[64];
     if (cudaError_t e = smem_limit_once(done, swapped_kernel); e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(g.mt * g.split));
-    cfg.blockDim = dim3(kI8Threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = g.split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = g.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, swapped_kernel, tw, tx, p, g);
+    return launch_chained(swapped_kernel, dim3((unsigned)(g.mt * g.split)), kI8Threads, smem, s, g.split, tw, tx, p, g);
 }
 
 }  // namespace
@@ -739,12 +730,12 @@ unsigned take_status_int8() { return take_tu_status(); }
 
 cudaError_t launch_linear_int8(const Int8Launch& p, cudaStream_t s, int sms) {
     if (p.M == 0) return cudaSuccess;
-    // One or two tokens: the dot form starts sooner (4096 x 4096: 3.4 and 3.8
-    // us against 5.7), but its warps walk long rows alone (4096 x 14336: 15.3
-    // against 13.5 us), and at two tokens it streams at 4.9 TB/s against 6
-    // (28672 x 4096: 24.1 against 21.6 us).
+    // One or two tokens: the dot form starts sooner (4096 x 4096: 3.1 and 3.4
+    // us against 4.7), but its warps walk long rows alone (4096 x 14336: 15
+    // against 13 us), and over a large weight it streams slower (28672 x 4096:
+    // 21.9 and 24.6 against 20.4 us; two tokens, 5120 x 5120: 6.0 against 5.2).
     const int64_t bytes = (int64_t)p.N * p.K;
-    if (p.K <= 8192 && (p.M == 1 || (p.M == 2 && bytes <= (64 << 20))))
+    if (p.K <= 8192 && p.M <= 2 && bytes <= (p.M == 1 ? 64 << 20 : 24 << 20))
         return p.M == 1 ? launch_dot<1>(p, s) : launch_dot<2>(p, s);
     // Up to 64 tokens, unless K is short: nothing to split, and the tiled form
     // has less to set up (48 x 1024 x 1024: 4.5 against 5.9 us).

@@ -144,6 +144,7 @@ residual_norm_kernel(const __grid_constant__ NormLaunch a, int stages) {
     const bool affine = a.gamma || a.scale, shifted = a.beta || a.shift;
     const bool scaled = a.post_gamma || a.gate || a.alpha != 1.0f;
     const uint32_t row_size = RING ? row_bytes(a) : 0;
+    chain_begin();
     if (RING) {
         if (tid == 0) {
             for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
@@ -350,6 +351,7 @@ residual_norm_fast_kernel(const __grid_constant__ NormLaunch a, int stages) {
     const int chunks = a.K >> 3;
     const bool last = (V - 1) * width + tid < chunks;     // of a thread's chunks only the last can lie past the row
     const uint32_t pitch_x = V * width * 8 * (XF32 ? 4 : 2), pitch = pitch_x + (H ? V * width * 16 : 0);
+    chain_begin();
     if (tid == 0) {
         for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
         fence_barrier_init();
@@ -534,8 +536,7 @@ cudaError_t launch_fast(const NormLaunch& p, int threads, cudaStream_t s, int sm
     static std::atomic<bool> done[64];
     if (cudaError_t e = ring_limit_once(done, kernel); e != cudaSuccess) return e;
     const unsigned grid = (unsigned)std::min<int64_t>(p.M, (int64_t)resident * sms);
-    kernel<<<grid, threads, stages * pitch, s>>>(p, stages);
-    return cudaGetLastError();
+    return launch_chained(kernel, dim3(grid), threads, stages * pitch, s, 1, p, stages);
 }
 
 template <int V, bool XF32>
@@ -580,14 +581,13 @@ cudaError_t launch_v(const NormLaunch& p, cudaStream_t s, int sms) {
     int resident = most;
     while (resident > 1 && kRingBytes / resident - 1024 < vecs + 2 * row) --resident;
     if (few || kRingBytes - 1024 < vecs + 2 * row || (mod && p.group_rows < (int64_t)2 * resident * sms)) {
-        residual_norm_kernel<V, XF32, false><<<(unsigned)p.M, threads, 0, s>>>(p, 0);
-        return cudaGetLastError();
+        return launch_chained(residual_norm_kernel<V, XF32, false>, dim3((unsigned)p.M), threads, 0, s, 1, p, 0);
     }
     const int stages = std::min(kMaxRing, (kRingBytes / resident - 1024 - vecs) / row);
     static std::atomic<bool> done[64];
     if (cudaError_t e = ring_limit_once(done, residual_norm_kernel<V, XF32, true>); e != cudaSuccess) return e;
-    residual_norm_kernel<V, XF32, true><<<(unsigned)(resident * sms), threads, stages * row + vecs, s>>>(p, stages);
-    return cudaGetLastError();
+    return launch_chained(residual_norm_kernel<V, XF32, true>, dim3((unsigned)(resident * sms)), threads,
+                          stages * row + vecs, s, 1, p, stages);
 }
 
 template <int V>

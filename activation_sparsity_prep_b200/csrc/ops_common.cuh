@@ -13,6 +13,17 @@ namespace sharq {
 
 constexpr unsigned kFull = 0xffffffffu;
 
+// Chained launches (launch_chained in ops_internal.h): a kernel may be placed
+// on the SMs while the one before it on its stream still runs.  chain_begin()
+// comes before a kernel's first access to memory that others write: it waits
+// until that kernel has ended and its writes are visible, and lets the next
+// one be placed.  What is set up before it (barriers, tensor memory, the
+// weight on its way into L2) costs no time after it.
+__device__ __forceinline__ void chain_begin() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 

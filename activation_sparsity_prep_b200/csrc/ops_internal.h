@@ -7,6 +7,29 @@
 
 namespace sharq {
 
+// Launches a kernel so that it may be placed on the SMs before the previous
+// kernel of its stream has ended; every kernel launched so begins with
+// chain_begin() (ops_common.cuh).  cluster: blocks of a cluster.
+template <class... P, class... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster,
+                           const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Rows of the residual stream: x' = x + alpha * gate * post(h), y = norm(x')
 // (see sharq_residual_norm in include/sharq.h).
 struct NormLaunch {

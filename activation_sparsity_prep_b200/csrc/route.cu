@@ -517,6 +517,7 @@ route_kernel(const __grid_constant__ RouteLaunch a) {
     __shared__ alignas(16) RouteScratch sh[kRouteWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float b[NPL];
+    chain_begin();
     const bool masks = load_bias(a, lane, b);
     for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.T; t += (int64_t)gridDim.x * kRouteWarps)
         route_token<NPL, SCORED, GROUPS>(a, t, lane, b, masks, route_smem + warp * a.E, sh[warp]);
@@ -667,12 +668,14 @@ __global__ void __launch_bounds__(kDispWarps * 32)
 dispatch_kernel(const DispatchLaunch a) {
     extern __shared__ int disp_smem[];
     __shared__ int wsum[32];
+    chain_begin();
     dispatch_body<C>(a, disp_smem, wsum);
 }
 
 __global__ void __launch_bounds__(256)
 invert_kernel(const DispatchLaunch a) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    chain_begin();
     if (i >= a.n) return;
     const int slot = a.position[i];
     if (slot >= 0) a.row_index[slot] = (int)((uint32_t)i / (uint32_t)a.k);
@@ -690,6 +693,7 @@ route_dispatch_kernel(const __grid_constant__ RouteLaunch r, const DispatchLaunc
     __shared__ int wsum[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float b[NPL];
+    chain_begin();
     const bool masks = load_bias(r, lane, b);
     for (int64_t t = warp; t < r.T; t += kDispWarps)
         route_token<NPL, SCORED, GROUPS>(r, t, lane, b, masks, route_smem + warp * r.E, sh[warp]);
@@ -716,19 +720,7 @@ cudaError_t launch_dispatch_c(const DispatchLaunch& p, cudaStream_t s) {
     static std::atomic<bool> done[64];
     if (cudaError_t e = allow_smem(done, dispatch_kernel<C>, dispatch_smem(kMaxRouteExperts), C > 8); e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C);
-    cfg.blockDim = dim3(kDispWarps * 32);
-    cfg.dynamicSmemBytes = dispatch_smem(p.E);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = C;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = C > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, dispatch_kernel<C>, p);
+    return launch_chained(dispatch_kernel<C>, dim3(C), kDispWarps * 32, dispatch_smem(p.E), s, C, p);
 }
 
 template <int NPL, bool SCORED, bool GROUPS>
@@ -741,13 +733,13 @@ cudaError_t launch_route_v(const RouteLaunch& p, const DispatchLaunch* order, cu
                                        (size_t)kDispWarps * kMaxRouteExperts * sizeof(double));
             e != cudaSuccess)
             return e;
-        route_dispatch_kernel<NPL, SCORED, GROUPS><<<1, kDispWarps * 32, smem, s>>>(p, *order);
-        return cudaGetLastError();
+        return launch_chained(route_dispatch_kernel<NPL, SCORED, GROUPS>, dim3(1), kDispWarps * 32, smem, s, 1, p, *order);
     }
     const int64_t blocks = std::min<int64_t>((p.T + kRouteWarps - 1) / kRouteWarps, (int64_t)sms * 12);
     const size_t smem = p.groups > 1 ? (size_t)kRouteWarps * p.E * sizeof(double) : 0;
-    route_kernel<NPL, SCORED, GROUPS><<<(unsigned)blocks, kRouteWarps * 32, smem, s>>>(p);
-    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (cudaError_t e = launch_chained(route_kernel<NPL, SCORED, GROUPS>, dim3((unsigned)blocks), kRouteWarps * 32, smem, s, 1, p);
+        e != cudaSuccess)
+        return e;
     return order ? launch_dispatch(*order, s) : cudaSuccess;
 }
 
@@ -803,6 +795,7 @@ __global__ void __launch_bounds__(256, J < 8 ? 0 : YF32 ? 2 : 4)
 combine_kernel(const CombineLaunch a) {
     const int64_t t = blockIdx.x;
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+    chain_begin();
     if (c >= a.N) return;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const int32_t* position = a.position + t * a.k;
@@ -846,10 +839,9 @@ cudaError_t launch_combine_t(const CombineLaunch& p, cudaStream_t s) {
     // 58.2 with 256)
     const int threads = std::min(64, (chunks + 31) / 32 * 32);
     const dim3 grid((unsigned)p.T, (unsigned)((chunks + threads - 1) / threads));
-    if (p.k <= 2)      combine_kernel<YF32, OF32, 2><<<grid, threads, 0, s>>>(p);
-    else if (p.k <= 4) combine_kernel<YF32, OF32, 4><<<grid, threads, 0, s>>>(p);
-    else               combine_kernel<YF32, OF32, 8><<<grid, threads, 0, s>>>(p);
-    return cudaGetLastError();
+    if (p.k <= 2) return launch_chained(combine_kernel<YF32, OF32, 2>, grid, threads, 0, s, 1, p);
+    if (p.k <= 4) return launch_chained(combine_kernel<YF32, OF32, 4>, grid, threads, 0, s, 1, p);
+    return launch_chained(combine_kernel<YF32, OF32, 8>, grid, threads, 0, s, 1, p);
 }
 
 }  // namespace
@@ -900,8 +892,7 @@ cudaError_t launch_dispatch(const DispatchLaunch& p, cudaStream_t s) {
     if (p.n <= 4096) return launch_dispatch_c<1>(p, s);
     cudaError_t e = p.n > 8 * 4096 && wide_cluster_fits() ? launch_dispatch_c<16>(p, s) : launch_dispatch_c<8>(p, s);
     if (e != cudaSuccess) return e;
-    invert_kernel<<<(unsigned)((p.n + 255) / 256), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_chained(invert_kernel, dim3((unsigned)((p.n + 255) / 256)), 256, 0, s, 1, p);
 }
 
 cudaError_t launch_combine(const CombineLaunch& p, cudaStream_t s) {
