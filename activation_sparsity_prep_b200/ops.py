@@ -63,15 +63,19 @@ def _declare(L: ctypes.CDLL) -> None:
 _lib = None
 
 
-def _call(name: str, *args) -> None:
+def _load() -> ctypes.CDLL:
     global _lib
-    from . import SharqError, load_sharq_ops
-    if _lib is None:
-        L = load_sharq_ops()
-        _declare(L)
-        _lib = L
-    st = getattr(_lib, name)(*args)
+    from . import load_sharq_ops
+    L = load_sharq_ops()
+    _declare(L)
+    _lib = L
+    return L
+
+
+def _call(name: str, *args) -> None:
+    st = getattr(_lib or _load(), name)(*args)
     if st != 0:
+        from . import SharqError
         raise SharqError(name, st)
 
 
@@ -334,7 +338,8 @@ def prepare_int8(X, gamma=None, eps: float = 1e-6, out: Optional[PreparedInt8] =
         if (out.M, out.K) != (M, K):
             raise ValueError(f"out describes M={out.M}, K={out.K}; the call needs M={M}, K={K}")
         _check_rows8("out", out, M, K, dev)
-    q = out if out is not None else PreparedInt8.empty(M, K, dev)
+    q = out if out is not None else PreparedInt8(torch.empty_like(X, dtype=torch.int8),
+                                                 torch.empty((M,), dtype=torch.float32, device=dev), M, K)
     c = _RowsInt8(q.codes.data_ptr(), q.scales.data_ptr(), M, K)
     _call("sharq_prepare_int8", X.data_ptr(), _ptr(gamma), eps, ctypes.byref(c), _stream(dev))
     return q
@@ -433,29 +438,32 @@ def residual_norm(x, h=None, norm: Optional[str] = "rms", post_gamma=None, gate=
             raise ValueError("gamma, beta, scale and shift need a norm")
         if int8 or out_y is not None:
             raise ValueError("int8 and out_y need a norm")
-    G, first = 1, None
-    for name, v in (("post_gamma", post_gamma), ("gamma", gamma), ("beta", beta)):
-        if v is not None:
-            _flat(name, v, (K,), _BF16_FP32, dev)
-            first = first or (name, v.dtype)
-            if v.dtype != first[1]:
-                raise ValueError(f"{name} is {v.dtype}, {first[0]} is {first[1]}")
-            setattr(a, name, v.data_ptr())
-    a.norm_is_fp32 = first is not None and first[1] == torch.float32
-    first = None
-    for name, v in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if v is not None:
-            if first is None:
-                if not isinstance(v, torch.Tensor) or v.dim() != 2:
-                    raise ValueError(f"{name} must be a 2-D tensor [G, K]")
-                first, G = (name, v.dtype), v.shape[0]
-                if G < 1 or M % G:
-                    raise ValueError(f"G={G} rows of {name} must divide M={M}")
-            setattr(a, "ld_" + name, _rows(name, v, (G, K), _BF16_FP32, dev))
-            if v.dtype != first[1]:
-                raise ValueError(f"{name} is {v.dtype}, {first[0]} is {first[1]}")
-            setattr(a, name, v.data_ptr())
-    a.mod_is_fp32 = first is not None and first[1] == torch.float32
+    if post_gamma is not None or gamma is not None or beta is not None:
+        first = None
+        for name, v in (("post_gamma", post_gamma), ("gamma", gamma), ("beta", beta)):
+            if v is not None:
+                _flat(name, v, (K,), _BF16_FP32, dev)
+                first = first or (name, v.dtype)
+                if v.dtype != first[1]:
+                    raise ValueError(f"{name} is {v.dtype}, {first[0]} is {first[1]}")
+                setattr(a, name, v.data_ptr())
+        a.norm_is_fp32 = first[1] == torch.float32
+    a.G = 1
+    if gate is not None or scale is not None or shift is not None:
+        first = None
+        for name, v in (("gate", gate), ("scale", scale), ("shift", shift)):
+            if v is not None:
+                if first is None:
+                    if not isinstance(v, torch.Tensor) or v.dim() != 2:
+                        raise ValueError(f"{name} must be a 2-D tensor [G, K]")
+                    first, G = (name, v.dtype), v.shape[0]
+                    if G < 1 or M % G:
+                        raise ValueError(f"G={G} rows of {name} must divide M={M}")
+                setattr(a, "ld_" + name, _rows(name, v, (G, K), _BF16_FP32, dev))
+                if v.dtype != first[1]:
+                    raise ValueError(f"{name} is {v.dtype}, {first[0]} is {first[1]}")
+                setattr(a, name, v.data_ptr())
+        a.G, a.mod_is_fp32 = G, first[1] == torch.float32
     if out_x is not None:
         a.ld_out = _rows("out_x", out_x, (M, K), (x.dtype,), dev)
         for name, v, ld in (("x", x, a.ld_x), ("h", h, a.ld_h)):
@@ -482,6 +490,6 @@ def residual_norm(x, h=None, norm: Optional[str] = "rms", post_gamma=None, gate=
                                                                  memory_format=torch.contiguous_format)
             a.y = y.data_ptr()
     a.x, a.x_is_fp32 = x.data_ptr(), x.dtype == torch.float32
-    a.M, a.G, a.K, a.norm, a.alpha, a.eps = M, G, K, _NORM[norm], alpha, eps
+    a.M, a.K, a.norm, a.alpha, a.eps = M, K, _NORM[norm], alpha, eps
     _call("sharq_residual_norm", ctypes.byref(a), _stream(dev))
     return out_x if out_x is not None else x, y
