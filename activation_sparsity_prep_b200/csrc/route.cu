@@ -254,6 +254,19 @@ __device__ __forceinline__ double quotient(double a, double b) { return a / b; }
 // 1 << group_shift lanes share a group: where a group is a power-of-two
 // number of whole lanes from their registers, else through shared memory,
 // each lane reading every p-th of the group's experts.
+
+// How many groups are better than this lane's group g with score `top`: larger,
+// or as large with a lower index.
+template <typename F>
+__device__ __forceinline__ int group_rank(F top, int g, const RouteLaunch& a) {
+    int rank = 0;
+    for (int h = 0; h < a.groups; ++h) {
+        const F v = __shfl_sync(kFull, top, h << a.group_shift);
+        rank += v > top || (v == top && h < g);
+    }
+    return rank;
+}
+
 template <int NPL, typename F>
 __device__ __forceinline__ bool keep_groups(const F (&of)[NPL], F (&key)[NPL], const RouteLaunch& a, int lane,
                                             bool inexact, float rel, F* scratch) {
@@ -291,19 +304,29 @@ __device__ __forceinline__ bool keep_groups(const F (&of)[NPL], F (&key)[NPL], c
     }
     if (a.group_top2 && second > F(kNegInf)) top += second;
     if (g >= a.groups) top = F(kNegInf);
-    // rank of this lane's group, equal groups by index
-    int rank = 0;
-#pragma unroll 4
-    for (int h = 0; h < a.groups; ++h) {
-        const F v = __shfl_sync(kFull, top, h << a.group_shift);
-        rank += v > top || (v == top && h < g);
-    }
+    // the groups not under the topk_groups-th largest score; where equal scores
+    // make them too many, by rank with the lower index first
     const bool live = top > F(kNegInf);
-    const bool kept = live && rank < a.topk_groups;
-    if (sizeof(F) == 4 && inexact) {
-        const float worst = -redux_max(kept ? -(float)top : kNegInf);
-        const float best = redux_max(live && !kept ? (float)top : kNegInf);
-        if (worst - best <= 4.0f * (2.0f * rel + 2.4e-7f * (1.0f + fabsf(worst)))) return false;
+    bool kept;
+    if constexpr (sizeof(F) == 4) {
+        float left = top, bound = kNegInf;
+        for (int r = 0; r < a.topk_groups; ++r) {
+            bound = redux_max(left);
+            if (left == bound) left = kNegInf;
+        }
+        kept = live && top >= bound;
+        if (inexact) {
+            const float best = redux_max(live && !kept ? top : kNegInf);
+            if (bound - best <= 4.0f * (2.0f * rel + 2.4e-7f * (1.0f + fabsf(bound)))) return false;
+        }
+        if (__popc(__ballot_sync(kFull, kept)) > a.topk_groups << a.group_shift) {
+            if (inexact) return false;
+            const int rank = group_rank(top, g, a);       // a warp step: outside any lane's condition
+            kept = live && rank < a.topk_groups;
+        }
+    } else {
+        const int rank = group_rank(top, g, a);
+        kept = live && rank < a.topk_groups;
     }
     if (a.group_whole) {
 #pragma unroll
@@ -322,6 +345,40 @@ __device__ __forceinline__ bool keep_groups(const F (&of)[NPL], F (&key)[NPL], c
 }
 
 enum Choice { kChosen, kTooClose, kTooMany };
+
+// Ranks of the gathered experts by score + bias in double: lane i < count has
+// expert e.  Not inlined: few tokens need it, and its registers would cost the
+// others theirs.
+template <int NPL>
+__device__ __noinline__ int exact_rank(const RouteLaunch* a, int64_t t, int lane, int count, int e, RouteScratch* sh) {
+    double score = 0.0, m = 0.0, sum = 1.0;
+    if (!a->sigmoid) {
+        float l[NPL], b[NPL];
+        load_logits(*a, t, lane, l);
+        load_bias(*a, lane, b);
+        float top = kNegInf;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            if (!(b[j] > kNegInf)) l[j] = kNegInf;
+            top = fmaxf(top, l[j]);
+        }
+        m = redux_max(top);
+        sum = 0.0;
+        for (int j = 0; j < NPL; ++j) sum += exp((double)l[j] - m);
+        sum = warp_sum(sum);
+    }
+    if (lane < count) {
+        const double x = logit_at(*a, t * a->ld + e);
+        score = (a->sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / sum) + (double)a->bias[e];
+    }
+    __syncwarp();
+    if (lane < count) sh->key[lane] = score;
+    __syncwarp();
+    int rank = 0;
+    for (int i = 0; i < count; ++i) rank += sh->key[i] > score || (sh->key[i] == score && i < lane);
+    __syncwarp();
+    return rank;
+}
 
 // The choice without a search round for each expert.  The k-th largest of the
 // 32 lane maxima bounds the k-th largest key from below, so the few keys not
@@ -402,7 +459,9 @@ __device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, i
         bound = redux_max(top);
         if (top == bound) top = kNegInf;                  // lanes with equal maxima go together: a lower bound still
     }
-    bound = fmaxf(bound, -3.4028235e38f);                 // masked keys stay out
+    // keys that fp32 may have put on the wrong side of the bound are gathered too
+    const float slack = kFp32 && scored ? 2.0f * rel + 2.4e-7f * (1.0f + fabsf(bound)) : 0.0f;
+    bound = fmaxf(bound - slack, -3.4028235e38f);         // masked keys stay out
     int n = 0;
 #pragma unroll
     for (int j = 0; j < NPL; ++j) n += (float)key[j] >= bound;
@@ -439,6 +498,18 @@ __device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, i
         }
         // equal keys (both zeros alike): the lower index first
         rank += __popc(__match_any_sync(kFull, __float_as_uint(v + 0.0f)) & ((1u << lane) - 1u));
+        if (scored) {
+            // neighbours in rank order; a score is at most 1
+            __syncwarp();
+            if (mine) gathered[rank] = v;
+            __syncwarp();
+            bool close = false;
+            if (lane < a.k && lane + 1 < count) {
+                const float p = (float)gathered[lane], q = (float)gathered[lane + 1];
+                close = p - q <= 2.0f * rel + 2.4e-7f * (1.0f + fmaxf(fabsf(p), fabsf(q)));
+            }
+            if (__any_sync(kFull, close)) rank = exact_rank<NPL>(&a, t, lane, count, e, &sh);
+        }
     } else {
         for (int i = 0; i < count; ++i) rank += gathered[i] > v || (gathered[i] == v && i < lane);
     }
@@ -457,18 +528,6 @@ __device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, i
             if (!kFp32 && need_all && exp_of(c - m) == F(0)) r = 0;      // every chosen score is 0
         }
         score = exp_of(x - c) * (!a.renormalize || r == F(0) ? r : F(1));
-    }
-    if (kFp32 && scored) {
-        // neighbours in rank order; a score is at most 1
-        __syncwarp();
-        if (mine) gathered[rank] = v;
-        __syncwarp();
-        bool close = false;
-        if (lane < a.k && lane + 1 < count) {
-            const float p = (float)gathered[lane], q = (float)gathered[lane + 1];
-            close = p - q <= 2.0f * rel + 2.4e-7f * (1.0f + fmaxf(fabsf(p), fabsf(q)));
-        }
-        if (__any_sync(kFull, close)) return kTooClose;
     }
     F w = chosen ? score : F(0);
     if (a.renormalize) {
@@ -580,9 +639,6 @@ __device__ __forceinline__ int block_scan(int v, int* wsum, int& sum) {
     return before + inc - v;
 }
 
-// C blocks share the choices; with C == 1 the block also writes row_index,
-// with more the scatter is left to invert_kernel, which has every SM's store
-// units (8 blocks alone took 9 us for 131072 rows).
 template <int C>
 __device__ __forceinline__ void dispatch_body(const DispatchLaunch& a, int* smem, int* wsum) {
     int* hist = smem;                             // [kDispWarps][E]
@@ -653,13 +709,12 @@ __device__ __forceinline__ void dispatch_body(const DispatchLaunch& a, int* smem
             __syncwarp();
             if (i < end) {
                 a.position[i] = slot;
-                if (C == 1 && slot >= 0) a.row_index[slot] = (int)((uint32_t)i / (uint32_t)a.k);
+                if (slot >= 0) a.row_index[slot] = (int)((uint32_t)i / (uint32_t)a.k);
             }
         }
     }
     // slots behind the last live one name row 0: valid rows of no expert
-    if (C == 1)
-        for (int64_t i = live + threadIdx.x; i < a.n; i += blockDim.x) a.row_index[i] = 0;
+    for (int64_t i = live + rank * blockDim.x + threadIdx.x; i < a.n; i += C * blockDim.x) a.row_index[i] = 0;
     if (C > 1) cluster_sync_all();                // no block leaves while its totals are read
 }
 
@@ -670,16 +725,6 @@ dispatch_kernel(const DispatchLaunch a) {
     __shared__ int wsum[32];
     chain_begin();
     dispatch_body<C>(a, disp_smem, wsum);
-}
-
-__global__ void __launch_bounds__(256)
-invert_kernel(const DispatchLaunch a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    chain_begin();
-    if (i >= a.n) return;
-    const int slot = a.position[i];
-    if (slot >= 0) a.row_index[slot] = (int)((uint32_t)i / (uint32_t)a.k);
-    if (i >= a.offsets[a.E]) a.row_index[i] = 0;
 }
 
 // Few tokens: the choice and the dispatch order by one block, in one launch.
@@ -887,12 +932,11 @@ bool wide_cluster_fits() {
 }  // namespace
 
 cudaError_t launch_dispatch(const DispatchLaunch& p, cudaStream_t s) {
-    // one block covers up to 4 choices a thread; beyond that a cluster does,
-    // of 16 blocks where the device places one
-    if (p.n <= 4096) return launch_dispatch_c<1>(p, s);
-    cudaError_t e = p.n > 8 * 4096 && wide_cluster_fits() ? launch_dispatch_c<16>(p, s) : launch_dispatch_c<8>(p, s);
-    if (e != cudaSuccess) return e;
-    return launch_chained(invert_kernel, dim3((unsigned)((p.n + 255) / 256)), 256, 0, s, 1, p);
+    // one block covers up to 2 choices a thread; beyond that a cluster does, of
+    // 16 blocks where the device places one (32768 choices: 6.5 us against 7.8
+    // with 8, 4800: 5.5 against 5.2; 4096 with one block 6.4)
+    if (p.n <= 2048) return launch_dispatch_c<1>(p, s);
+    return p.n > 8192 && wide_cluster_fits() ? launch_dispatch_c<16>(p, s) : launch_dispatch_c<8>(p, s);
 }
 
 cudaError_t launch_combine(const CombineLaunch& p, cudaStream_t s) {
