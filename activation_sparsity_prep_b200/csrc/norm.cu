@@ -11,8 +11,8 @@
 // One block works on a row at a time and holds it in registers from the load
 // to the stores, so every input is read once and every output written once;
 // the kernel is bound by memory.  All statistics are fp32 over the unrounded x',
-// reduced in an order that depends on K alone: a row's result does not
-// depend on the rows around it.
+// reduced in an order that depends on K and on the parts of the call: a row's
+// result does not depend on the rows around it.
 #include <algorithm>
 #include <atomic>
 

@@ -140,9 +140,8 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
-// Bounded wait.  mbar_wait() reads the global timer as soon as a first try
-// fails, and that read takes longer than a k-step; a try suspends the thread
-// by itself, so a few hundred of them come first.
+// Bounded wait: a few hundred tries, each of which suspends the thread by
+// itself, then mbar_wait(), which times them by the global timer.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
     for (int i = 0; i < 256; ++i)

@@ -248,13 +248,6 @@ __device__ __forceinline__ double fast_exp(double v) { return exp(v); }
 __device__ __forceinline__ float quotient(float a, float b) { return __fdividef(a, b); }
 __device__ __forceinline__ double quotient(double a, double b) { return a / b; }
 
-// Masks the keys outside the groups that a token may use; `of` holds what a
-// group's score is made of.  Returns false when the last kept and the first
-// dropped group are too close for fp32 (checked where scores are inexact).
-// 1 << group_shift lanes share a group: where a group is a power-of-two
-// number of whole lanes from their registers, else through shared memory,
-// each lane reading every p-th of the group's experts.
-
 // How many groups are better than this lane's group g with score `top`: larger,
 // or as large with a lower index.
 template <typename F>
@@ -267,6 +260,12 @@ __device__ __forceinline__ int group_rank(F top, int g, const RouteLaunch& a) {
     return rank;
 }
 
+// Masks the keys outside the groups that a token may use; `of` holds what a
+// group's score is made of.  Returns false when the last kept and the first
+// dropped group are too close for fp32 (checked where scores are inexact).
+// 1 << group_shift lanes share a group: where a group is a power-of-two
+// number of whole lanes from their registers, else through shared memory,
+// each lane reading every p-th of the group's experts.
 template <int NPL, typename F>
 __device__ __forceinline__ bool keep_groups(const F (&of)[NPL], F (&key)[NPL], const RouteLaunch& a, int lane,
                                             bool inexact, float rel, F* scratch) {
@@ -383,10 +382,11 @@ __device__ __noinline__ int exact_rank(const RouteLaunch* a, int64_t t, int lane
 // The choice without a search round for each expert.  The k-th largest of the
 // 32 lane maxima bounds the k-th largest key from below, so the few keys not
 // under it are gathered, in expert order, and ranked against one another.
-// The kernel is bound by instruction issue: 16383 tokens of 256 experts took
-// 13.8 M warp instructions and 25 us with search rounds (sigmoid with bias).
-// F = float leaves close decisions to F = double (kTooClose), which gathers
-// on its keys rounded to fp32, an order-preserving step, and ranks the keys
+// The kernel is bound by instruction issue: 16383 tokens of 256 experts, sigmoid
+// with bias, took 13.8 M warp instructions and 30 us with search rounds, and
+// take 10.6 M and 16 us so.  F = float ranks close candidates in double, and
+// leaves close groups and underflow to F = double (kTooClose), which gathers on
+// its keys rounded to fp32, an order-preserving step, and ranks the keys
 // themselves.  Nothing is written unless kChosen is returned.
 template <int NPL, bool SCORED, bool GROUPS, typename F>
 __device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, int lane, const float (&b)[NPL],
