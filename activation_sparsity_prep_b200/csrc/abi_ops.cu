@@ -17,6 +17,7 @@ bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p)
 
 sharq_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return SHARQ_OK;
+    cudaGetLastError();                       // reported here: not left for the caller's next check
     if (e == cudaErrorNotSupported) return SHARQ_ERR_UNSUPPORTED;
     return SHARQ_ERR_CUDA;
 }

@@ -229,8 +229,8 @@ __device__ __forceinline__ bool produce(const CUtensorMap* ta, const CUtensorMap
     return true;
 }
 
-// Waits (bounded) for the loads still in flight after an early end: those of
-// the stages behind the last one issued whose phase has not completed.
+// Waits (bounded) for the loads still in flight after an early end: each stage's
+// last issued phase.
 __device__ __forceinline__ void drain(I8Barriers* bars, int stages, Ring at, bool wrapped) {
     for (int i = 0; i < stages; ++i) {
         const uint32_t parity = i < (int)at.s ? at.phase : at.phase ^ 1;

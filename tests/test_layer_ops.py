@@ -172,6 +172,51 @@ def test_captured_and_replayed(T):
     assert sq.last_device_status() == 0
 
 
+def test_streams_joined_by_events_eager_and_captured():
+    """Work forked to a side stream and joined again: a call after the join
+    sees what both wrote, also where it is placed early."""
+    g = gen(31)
+    w = sq.quantize_weight_int8(randn(g, 1040, 512, scale=0.05))
+    w2 = sq.quantize_weight_int8(randn(g, 512, 1040, scale=0.05))
+    x, h = randn(g, 300, 512), randn(g, 300, 512)
+    side = torch.cuda.Stream()
+    big = torch.randn((4096, 4096), device="cuda")
+
+    def forked():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            slow = big @ big                                  # the side stream's result comes late
+            hs = h * (1.0 + 0.0 * slow[0, 0]).to(BF)
+            y = sq.linear_int8(sq.prepare_int8(hs), w)
+        a, q = sq.residual_norm(x, h, int8=True)
+        z = sq.linear_int8(q, w)
+        main.wait_stream(side)
+        _, q2 = sq.residual_norm(y, z, int8=True)
+        out, _ = sq.residual_norm(a, sq.linear_int8(q2, w2))
+        return a, y, z, out
+
+    a, q = sq.residual_norm(x, h, int8=True)
+    z = sq.linear_int8(q, w)
+    y = sq.linear_int8(sq.prepare_int8(h), w)
+    torch.cuda.synchronize()
+    _, q2 = sq.residual_norm(y, z, int8=True)
+    want = (a, y, z, sq.residual_norm(a, sq.linear_int8(q2, w2))[0])
+    for _ in range(5):
+        got = forked()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        got = forked()
+    for _ in range(5):
+        for t in got:
+            t.zero_()
+        gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_first_calls_inside_a_capture():
     """A process whose first call of every operator is captured."""
     code = """
