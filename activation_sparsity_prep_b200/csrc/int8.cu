@@ -9,7 +9,7 @@
 // Three forms:
 //   dot     one or two tokens: a warp for two or four channels on the
 //           dot-product units, bound by streaming the weight;
-//   swapped up to 64 tokens: 128 channels x all tokens on the tensor cores
+//   swapped up to 64 tokens (128 in narrow, long layers): 128 channels x all tokens on the tensor cores
 //           (the weight is the M-side operand), K split over a cluster so
 //           that narrow layers use every SM; bound by the weight;
 //   tiled   128 or 256 tokens x up to 256 channels a tile, persistent, bound
@@ -100,7 +100,7 @@ constexpr int kStep = 128;                    // K a pipeline stage: one 128-byt
 constexpr uint32_t kABytes = kRows * kStep;
 constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;                  // blocks of a cluster that share a tile's K
-constexpr int kSwappedTokens = 64;            // most tokens of the swapped form
+constexpr int kSwappedTokens = 128;           // most tokens of the swapped form
 constexpr int kI8Threads = 192;               // TMA warp, MMA warp, four epilogue warps
 
 struct alignas(8) I8Barriers {
@@ -172,6 +172,7 @@ __host__ __device__ constexpr uint32_t i8_idesc(int n, int m = kRows) {
 struct Geometry {
     int bn;                  // rows of the N-side operand of a tile
     int stages;
+    int sub;                 // k-steps a stage
     int mt, nt;              // tiles along the M-side and the N-side operand
     int bn2, nt2;            // tiled form: narrower tiles behind the nt of width bn, or none
     int n_fast;              // tile walk: N-side fastest
@@ -204,24 +205,27 @@ struct Ring {
     }
 };
 
-// Issues the TMA loads of k-steps [k0, k1) of one tile.  PAIR: both blocks'
-// loads complete on the even block's barrier, which expects the bytes of both.
+// Issues the TMA loads of k-steps [k0, k1) of one tile, `sub` a stage, each
+// k-step `bytes` into its `block` of the stage.  PAIR: both blocks' loads
+// complete on the even block's barrier, which expects the bytes of both.
 template <bool PAIR>
 __device__ __forceinline__ bool produce(const CUtensorMap* ta, const CUtensorMap* tb, I8Barriers* bars, uint8_t* smem,
-                                        uint32_t stride, uint32_t bytes, int stages, Ring& at, int k0, int k1, int arow, int brow,
-                                        bool lead = true) {
-    for (int k = k0; k < k1; ++k, at.next(stages)) {
+                                        uint32_t block, uint32_t bytes, const Geometry& g, Ring& at, int k0, int k1,
+                                        int arow, int brow, bool lead = true) {
+    for (int k = k0; k < k1; k += g.sub, at.next(g.stages)) {
         if (!__all_sync(kFull, wait_bar(&bars->empty[at.s], at.phase ^ 1))) return false;
-        uint8_t* st = smem + at.s * stride;
+        uint8_t* st = smem + at.s * g.sub * block;
+        const int n = min(g.sub, k1 - k);
         if (elect_one()) {
-            if constexpr (PAIR) {
-                if (lead) mbar_arrive_expect_tx(&bars->full[at.s], 2 * bytes);
-                tma_load_2d_pair(st, ta, &bars->full[at.s], k * kStep, arow);
-                tma_load_2d_pair(st + kABytes, tb, &bars->full[at.s], k * kStep, brow);
-            } else {
-                mbar_arrive_expect_tx(&bars->full[at.s], bytes);
-                tma_load_2d(st, ta, &bars->full[at.s], k * kStep, arow);
-                tma_load_2d(st + kABytes, tb, &bars->full[at.s], k * kStep, brow);
+            if (!PAIR || lead) mbar_arrive_expect_tx(&bars->full[at.s], (PAIR ? 2 : 1) * n * bytes);
+            for (int i = 0; i < n; ++i, st += block) {
+                if constexpr (PAIR) {
+                    tma_load_2d_pair(st, ta, &bars->full[at.s], (k + i) * kStep, arow);
+                    tma_load_2d_pair(st + kABytes, tb, &bars->full[at.s], (k + i) * kStep, brow);
+                } else {
+                    tma_load_2d(st, ta, &bars->full[at.s], (k + i) * kStep, arow);
+                    tma_load_2d(st + kABytes, tb, &bars->full[at.s], (k + i) * kStep, brow);
+                }
             }
         }
         __syncwarp();
@@ -240,17 +244,21 @@ __device__ __forceinline__ void drain(I8Barriers* bars, int stages, Ring at, boo
 
 // Multiplies nk staged k-steps into the accumulator at tensor-memory address d.
 template <bool PAIR>
-__device__ __forceinline__ bool multiply(I8Barriers* bars, uint64_t desc0, uint32_t stride, int stages, Ring& at,
+__device__ __forceinline__ bool multiply(I8Barriers* bars, uint64_t desc0, uint32_t block, const Geometry& g, Ring& at,
                                          int nk, uint32_t d, uint32_t idesc) {
-    for (int k = 0; k < nk; ++k, at.next(stages)) {
+    for (int k = 0; k < nk; k += g.sub, at.next(g.stages)) {
         if (!__all_sync(kFull, wait_bar(&bars->full[at.s], at.phase))) return false;
         tc_fence_after();
-        const uint64_t da = desc0 + at.s * (stride >> 4), db = da + (kABytes >> 4);
+        const uint64_t stage = desc0 + at.s * (g.sub * block >> 4);
+        const int n = min(g.sub, nk - k);
         if (elect_one()) {
+            for (int i = 0; i < n; ++i) {
+                const uint64_t da = stage + i * (block >> 4), db = da + (kABytes >> 4);
 #pragma unroll
-            for (int j = 0; j < kStep / 32; ++j) {
-                if constexpr (PAIR) tc_mma_i8_pair(d, da + 2 * j, db + 2 * j, idesc, (k | j) ? 1u : 0u);
-                else                tc_mma_i8(d, da + 2 * j, db + 2 * j, idesc, (k | j) ? 1u : 0u);
+                for (int j = 0; j < kStep / 32; ++j) {
+                    if constexpr (PAIR) tc_mma_i8_pair(d, da + 2 * j, db + 2 * j, idesc, (k | i | j) ? 1u : 0u);
+                    else                tc_mma_i8(d, da + 2 * j, db + 2 * j, idesc, (k | i | j) ? 1u : 0u);
+                }
             }
             if constexpr (PAIR) tc_commit_pair(&bars->empty[at.s]);
             else                tc_commit(&bars->empty[at.s]);
@@ -261,10 +269,10 @@ __device__ __forceinline__ bool multiply(I8Barriers* bars, uint64_t desc0, uint3
 }
 
 template <bool PAIR>
-__device__ __forceinline__ uint8_t* setup(uint8_t* raw, const Geometry& g, uint32_t stride, I8Barriers*& bars,
+__device__ __forceinline__ uint8_t* setup(uint8_t* raw, const Geometry& g, uint32_t block, I8Barriers*& bars,
                                           uint8_t*& tail) {
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    tail = smem + g.stages * stride;
+    tail = smem + g.stages * g.sub * block;
     bars = reinterpret_cast<I8Barriers*>(tail);
     tail += (sizeof(I8Barriers) + 127) / 128 * 128;
     if (threadIdx.x == 0) {
@@ -315,10 +323,10 @@ tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUt
              const __grid_constant__ CUtensorMap tb2, const Int8Launch a, const Geometry g) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     constexpr int kShare = PAIR ? 2 : 1;                  // blocks that share a tile's channels
-    const uint32_t stride = kABytes + g.bn / kShare * kStep;
+    const uint32_t block = kABytes + g.bn / kShare * kStep;
     I8Barriers* bars;
     uint8_t* tail;
-    uint8_t* smem = setup<PAIR>(smem_raw, g, stride, bars, tail);
+    uint8_t* smem = setup<PAIR>(smem_raw, g, block, bars, tail);
     const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t tmem = __shfl_sync(kFull, bars->tmem_base, 0);
     const int nk = (a.K + kStep - 1) / kStep;
@@ -336,8 +344,8 @@ tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUt
         for (int t = first; t < tiles; t += step, done = 1) {
             const Tile w = tile_at(g, t);
             const int brows = w.width / kShare;           // channels that this block loads
-            if (!produce<PAIR>(&ta, w.width == g.bn ? &tb : &tb2, bars, smem, stride, kABytes + brows * kStep, g.stages,
-                               at, 0, nk, w.m * kTileRows + rank * kRows, w.col + rank * brows, rank == 0)) {
+            if (!produce<PAIR>(&ta, w.width == g.bn ? &tb : &tb2, bars, smem, block, kABytes + brows * kStep, g, at, 0, nk,
+                               w.m * kTileRows + rank * kRows, w.col + rank * brows, rank == 0)) {
                 if (rank == 0) drain(bars, g.stages, at, done || at.phase);
                 break;
             }
@@ -350,7 +358,7 @@ tiled_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUt
             const uint32_t buf = tc & 1, use = tc >> 1;
             if (use > 0 && !__all_sync(kFull, wait_bar(&bars->acc_empty[buf], (use - 1) & 1))) break;
             tc_fence_after();
-            if (!multiply<PAIR>(bars, desc0, stride, g.stages, at, nk, tmem + buf * g.bn, i8_idesc(tile_at(g, t).width, kTileRows)))
+            if (!multiply<PAIR>(bars, desc0, block, g, at, nk, tmem + buf * g.bn, i8_idesc(tile_at(g, t).width, kTileRows)))
                 break;
             if (elect_one()) {
                 if constexpr (PAIR) tc_commit_pair(&bars->acc_full[buf]);
@@ -472,10 +480,10 @@ __global__ void __launch_bounds__(kI8Threads)
 swapped_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const Int8Launch a,
                const Geometry g) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t stride = kABytes + g.bn * kStep;
+    const uint32_t block = kABytes + g.bn * kStep;
     I8Barriers* bars;
     uint8_t* tail;
-    uint8_t* smem = setup<false>(smem_raw, g, stride, bars, tail);
+    uint8_t* smem = setup<false>(smem_raw, g, block, bars, tail);
     const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t tmem = __shfl_sync(kFull, bars->tmem_base, 0);
     const int nk = (a.K + kStep - 1) / kStep;
@@ -496,11 +504,11 @@ swapped_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
 
     if (warp == 0) {
         Ring at{0, 0};
-        if (!produce<false>(&tw, &tx, bars, smem, stride, stride, g.stages, at, k0, k1, tile * kRows, 0))
+        if (!produce<false>(&tw, &tx, bars, smem, block, block, g, at, k0, k1, tile * kRows, 0))
             drain(bars, g.stages, at, at.phase);
     } else if (warp == 1) {
         Ring at{0, 0};
-        if (multiply<false>(bars, sdesc_sw128(smem_u32(smem)), stride, g.stages, at, k1 - k0, tmem, i8_idesc(g.bn)) && elect_one())
+        if (multiply<false>(bars, sdesc_sw128(smem_u32(smem)), block, g, at, k1 - k0, tmem, i8_idesc(g.bn)) && elect_one())
             tc_commit(&bars->acc_full[0]);
     }
     __syncwarp();
@@ -633,9 +641,12 @@ cudaError_t launch_tiled_t(const CUtensorMap& ta, const CUtensorMap& tb, const C
 }
 
 // Time of a tile of this width a k-step, in units of 1.3 ns, measured over 128
-// k-steps: pairs of blocks 156, 176, 237, 313 ns for 64 to 256 channels,
-// single blocks (half as many rows) 148, 220, 297, 396 ns.
-int64_t tile_cost(bool pair, int bn) { return pair ? std::max(121, 30 + bn * 83 / 100) : bn + 47; }
+// k-steps: pairs of blocks 113, 176, 237, 313 ns for 64 to 256 channels,
+// single blocks (half as many rows) 120, 220, 297, 396 ns.
+int64_t tile_cost(bool pair, int bn) {
+    if (bn == 64) return pair ? 88 : 92;
+    return pair ? 30 + bn * 83 / 100 : bn + 47;
+}
 
 // Shape and order of the tiles.  All of one width, or 256 wide for as many
 // whole waves as there are and narrower behind, so that a last wave of a few
@@ -680,7 +691,11 @@ cudaError_t launch_tiled(const Int8Launch& p, cudaStream_t s, int sms) {
     g.split = 1;
     g.tmem_cols = tmem_cols(2 * g.bn);
     const int share = pair ? 2 : 1;
-    const uint32_t stride = kABytes + g.bn / share * kStep;
+    // the narrowest tiles: two k-steps a stage, half the barrier steps for their
+    // MMAs (128 k-steps of 64 channels: 30.6 -> 25.0 us, pairs 35.2 -> 25.8; no
+    // gain from 128 channels on, where fewer stages cost more)
+    g.sub = g.bn <= 64 ? 2 : 1;
+    const uint32_t stride = g.sub * (kABytes + g.bn / share * kStep);
     g.stages = std::min<int>(kMaxStages, (int)((227 * 1024 - 1024 - kBarBytes - kEpilogueBytes) / stride));
     const size_t smem = 1024 + g.stages * stride + kBarBytes + kEpilogueBytes;
     CUtensorMap ta, tb, tb2;
@@ -705,6 +720,7 @@ cudaError_t launch_swapped(const Int8Launch& p, cudaStream_t s, int sms) {
     g.bn = (int)((p.M + 15) / 16 * 16);
     g.mt = (p.N + kRows - 1) / kRows;
     g.nt = 1;
+    g.sub = 1;
     g.tmem_cols = tmem_cols(g.bn);
     const int nk = (p.K + kStep - 1) / kStep;
     // fewer tiles than SMs: split K so that a cluster of blocks shares a
@@ -715,7 +731,8 @@ cudaError_t launch_swapped(const Int8Launch& p, cudaStream_t s, int sms) {
     constexpr uint32_t kExtra = kBarBytes + kSwappedTokens * 4;
     const uint32_t room = 112 * 1024 - 1024 - kExtra;
     g.stages = std::min<int>({kMaxStages, (int)(room / stride), std::max(2, (nk + g.split - 1) / g.split)});
-    // the partial tiles, bn x 512 bytes, lie over the stages (bn <= 64: two hold 36 KB or more)
+    // the partial tiles, bn x 512 bytes, lie over the stages: two stages of 16 KB
+    // and bn x 128 bytes hold them up to bn = 128
     const size_t smem = 1024 + g.stages * stride + kExtra;
     CUtensorMap tw, tx;
     if (!make_map(&tw, p.w, p.N, p.K, kRows) || !make_map(&tx, p.x, p.M, p.K, g.bn)) return cudaErrorInvalidValue;
@@ -738,8 +755,10 @@ cudaError_t launch_linear_int8(const Int8Launch& p, cudaStream_t s, int sms) {
     if (p.K <= 8192 && p.M <= 2 && bytes <= (p.M == 1 ? 64 << 20 : 24 << 20))
         return p.M == 1 ? launch_dot<1>(p, s) : launch_dot<2>(p, s);
     // Up to 64 tokens, unless K is short: nothing to split, and the tiled form
-    // has less to set up (48 x 1024 x 1024: 4.5 against 5.9 us).
-    if (p.M <= kSwappedTokens && p.K > 1024) return launch_swapped(p, s, sms);
+    // has less to set up (48 x 1024 x 1024: 4.5 against 5.9 us).  Up to 128 where
+    // K is long and there are too few channels for tiles on every SM (128 x 4096
+    // x 14336: 18.1 against 20.3 us).
+    if (p.K > 1024 && p.M <= (p.K >= 8192 && p.N <= 64 * sms / 2 ? kSwappedTokens : 64)) return launch_swapped(p, s, sms);
     return launch_tiled(p, s, sms);
 }
 
