@@ -591,16 +591,18 @@ route_kernel(const __grid_constant__ RouteLaunch a) {
 // ranked by a warp match, so the order is fixed; no workspace.
 constexpr int kDispWarps = 32;
 constexpr int kBatch = 8;            // groups of 32 choices whose loads are in flight together
+constexpr int kHeld = 2;             // groups of a run short enough to stay in registers
 
 // ids[first + 32 b + lane], -1 where there is none or no such expert
-__device__ __forceinline__ void load_batch(const DispatchLaunch& a, int64_t at, int64_t end, int lane, int (&e)[kBatch]) {
+template <int B>
+__device__ __forceinline__ void load_batch(const DispatchLaunch& a, int64_t at, int64_t end, int lane, int (&e)[B]) {
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
+    for (int b = 0; b < B; ++b) {
         const int64_t i = at + b * 32 + lane;
         e[b] = i < end ? a.ids[i] : -1;
     }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b)
+    for (int b = 0; b < B; ++b)
         if ((unsigned)e[b] >= (unsigned)a.E) e[b] = -1;
 }
 
@@ -654,12 +656,30 @@ __device__ __forceinline__ void dispatch_body(const DispatchLaunch& a, int* smem
 
     for (int i = threadIdx.x; i < kDispWarps * a.E; i += blockDim.x) hist[i] = 0;
     __syncthreads();
-    for (int64_t at = first; at < end; at += kBatch * 32) {
-        int e[kBatch];
-        load_batch(a, at, end, lane, e);
+    // a short run is ranked as it is counted and stays in registers; a longer
+    // one is counted now and walked again, its ranks under its stores (131064
+    // choices: 11.6 against 14.9 us held, 2048: 3.2 against 3.0)
+    const bool once = per <= kHeld * 32;
+    int held[kHeld], local[kHeld];
+    if (once) {
+        load_batch(a, first, end, lane, held);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-            if (e[b] >= 0) atomicAdd(&mine[e[b]], 1);     // counts only: their order does not matter
+        for (int b = 0; b < kHeld; ++b) {
+            if (first + b * 32 >= end) break;
+            const unsigned peers = same_expert(held[b], bits);
+            if (held[b] >= 0) local[b] = mine[held[b]] + __popc(peers & ((1u << lane) - 1u));
+            __syncwarp();
+            if (held[b] >= 0 && lane == __ffs(peers) - 1) mine[held[b]] += __popc(peers);
+            __syncwarp();
+        }
+    } else {
+        for (int64_t at = first; at < end; at += kBatch * 32) {
+            int e[kBatch];
+            load_batch(a, at, end, lane, e);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (e[b] >= 0) atomicAdd(&mine[e[b]], 1);     // counts only: their order does not matter
+        }
     }
     __syncthreads();
     // exclusive scan of each expert's counts over the block's warps
@@ -694,22 +714,32 @@ __device__ __forceinline__ void dispatch_body(const DispatchLaunch& a, int* smem
     }
     if (rank == 0 && threadIdx.x == 0) a.offsets[a.E] = live;
     __syncthreads();
-    for (int64_t at = first; at < end; at += kBatch * 32) {
-        int e[kBatch];
-        load_batch(a, at, end, lane, e);
+    auto place = [&](int64_t i, int slot) {
+        if (i < end) {
+            a.position[i] = slot;
+            if (slot >= 0) a.row_index[slot] = (int)((uint32_t)i / (uint32_t)a.k);
+        }
+    };
+    if (once) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            if (at + b * 32 >= end) break;
-            const int64_t i = at + b * 32 + lane;
-            const unsigned peers = same_expert(e[b], bits);
-            int slot = -1;
-            if (e[b] >= 0) slot = start[e[b]] + mine[e[b]] + __popc(peers & ((1u << lane) - 1u));
-            __syncwarp();
-            if (e[b] >= 0 && lane == __ffs(peers) - 1) mine[e[b]] += __popc(peers);
-            __syncwarp();
-            if (i < end) {
-                a.position[i] = slot;
-                if (slot >= 0) a.row_index[slot] = (int)((uint32_t)i / (uint32_t)a.k);
+        for (int b = 0; b < kHeld; ++b) {
+            if (first + b * 32 >= end) break;
+            place(first + b * 32 + lane, held[b] >= 0 ? start[held[b]] + mine[held[b]] + local[b] : -1);
+        }
+    } else {
+        for (int64_t at = first; at < end; at += kBatch * 32) {
+            int e[kBatch];
+            load_batch(a, at, end, lane, e);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (at + b * 32 >= end) break;
+                const unsigned peers = same_expert(e[b], bits);
+                int slot = -1;
+                if (e[b] >= 0) slot = start[e[b]] + mine[e[b]] + __popc(peers & ((1u << lane) - 1u));
+                __syncwarp();
+                if (e[b] >= 0 && lane == __ffs(peers) - 1) mine[e[b]] += __popc(peers);
+                __syncwarp();
+                place(at + b * 32 + lane, slot);
             }
         }
     }
