@@ -21,8 +21,9 @@ def route(logits, k, score="softmax", bias=None, groups=1, topk_groups=1, group_
                 s[e] = np.exp(logits[t, e] - m)
             s /= s.sum()
         elif score == "sigmoid":
-            for e in live:
-                s[e] = 1.0 / (1.0 + np.exp(-logits[t, e]))
+            with np.errstate(over="ignore"):
+                for e in live:
+                    s[e] = 1.0 / (1.0 + np.exp(-logits[t, e]))
         # without a bias the order of the scores is that of the logits
         c = {e: s[e] + b[e] for e in live}
         order = c if bias is not None else {e: logits[t, e] for e in live}

@@ -276,6 +276,52 @@ def test_other_streams_at_once():
     assert c.shape == (200, 512)
 
 
+@pytest.mark.slow
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: their last rows against the same
+    rows alone."""
+    g = gen(41)
+    M, K = 540000, 4096                                      # 2.2e9 elements
+    x, h = torch.zeros((M, K), dtype=BF, device="cuda"), torch.zeros((M, K), dtype=BF, device="cuda")
+    x[-3:], h[-3:] = randn(g, 3, K), randn(g, 3, K)
+    gm = (0.5 + torch.rand(K, generator=g, device="cuda")).to(BF)
+    xo, y = sq.residual_norm(x, h, gamma=gm)
+    x1, y1 = sq.residual_norm(x[-3:], h[-3:], gamma=gm)
+    assert torch.equal(xo[-3:], x1) and torch.equal(y[-3:], y1) and not y[:5].any()
+    del xo, y
+    _, q = sq.residual_norm(x, h, gamma=gm, int8=True)
+    _, q1 = sq.residual_norm(x[-3:], h[-3:], gamma=gm, int8=True)
+    assert torch.equal(q.codes[-3:], q1.codes) and torch.equal(q.scales[-3:], q1.scales)
+    # experts' rows behind 2^31 elements
+    pos = torch.tensor([[M - 1, M - 3], [M - 2, 0]], dtype=torch.int32, device="cuda")
+    w = torch.rand((2, 2), generator=g, device="cuda")
+    near = torch.cat((x[:1], x[-3:]))
+    assert torch.equal(sq.moe_combine(x, pos, w), sq.moe_combine(near, torch.tensor([[3, 1], [2, 0]], dtype=torch.int32,
+                                                                                    device="cuda"), w))
+    # a product whose operand and whose result pass it
+    w8 = sq.quantize_weight_int8(randn(g, 264, K, scale=0.05))
+    assert torch.equal(sq.linear_int8(q, w8)[-3:], sq.linear_int8(q1, w8))
+    del x, h, q
+    a = sq.prepare_int8(randn(g, 36000, 32))
+    b = sq.quantize_weight_int8(randn(g, 60008, 32))
+    out = sq.linear_int8(a, b)                               # 2.2e9 elements
+    tail = sq.PreparedInt8(a.codes[-2:].clone(), a.scales[-2:].clone(), 2, 32)
+    assert torch.equal(out[-2:], sq.linear_int8(tail, b))
+    wt = sq.WeightInt8(b.codes[-8:].clone(), b.scales[-8:].clone(), 8, 32)
+    assert torch.equal(out[:, -8:], sq.linear_int8(a, wt))
+    del out
+    # a long weight for one token
+    one = sq.prepare_int8(randn(g, 1, 4096))
+    big = sq.WeightInt8(torch.zeros((540000, 4096), dtype=torch.int8, device="cuda"), torch.ones(540000, device="cuda"), 540000, 4096)
+    big.codes[-1] = 1
+    y = sq.linear_int8(one, big, out_fp32=True)
+    assert float(y[0, -1]) != 0 and not y[0, :-1].any()
+    want = float(one.codes.double().sum()) * float(one.scales[0])
+    assert abs(float(y[0, -1]) - want) <= 4 * 2.0 ** -24 * abs(want)
+    torch.cuda.synchronize()
+    assert sq.last_device_status() == 0
+
+
 # ------------------------------------------------------------- guarded ----
 
 GUARD = 4096
