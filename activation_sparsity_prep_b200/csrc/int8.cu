@@ -723,9 +723,20 @@ cudaError_t launch_swapped(const Int8Launch& p, cudaStream_t s, int sms) {
     g.sub = 1;
     g.tmem_cols = tmem_cols(g.bn);
     const int nk = (p.K + kStep - 1) / kStep;
-    // fewer tiles than SMs: split K so that a cluster of blocks shares a
-    // tile, each keeping at least 4 k-steps
-    g.split = std::max(1, std::min({kMaxSplit, nk / 4, std::max(1, sms) / g.mt}));
+    // Fewer tiles than SMs: split K over a cluster, each block keeping at least
+    // 4 k-steps: the split that leaves an SM the fewest k-steps, one block or two
+    // to the SM, where clusters fill about seven eighths of the places and their
+    // sum costs a few k-steps (6144 x 4096: 144 blocks in clusters of three take
+    // 7.5 us, 96 in pairs 6.2; 10240 x 8192: 80 blocks 19.3 us, 240 in clusters
+    // of three 15.8; 12288 x 4096: 96 blocks 12.1 us, 768 in eights 14.4).
+    g.split = 1;
+    const int places = sms * 7 / 8;
+    int least = 2 * nk;
+    for (int split = 2; split <= std::min(kMaxSplit, nk / 4) && g.mt * split <= 2 * places; ++split) {
+        const int held = g.mt * split <= places ? 1 : 2;
+        const int cost = 2 * held * ((nk + split - 1) / split) + 6 + split;
+        if (cost < least) { least = cost; g.split = split; }
+    }
     const uint32_t stride = kABytes + g.bn * kStep;
     // two blocks an SM: one loads while the other finishes
     constexpr uint32_t kExtra = kBarBytes + kSwappedTokens * 4;
