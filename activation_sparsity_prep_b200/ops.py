@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
@@ -86,17 +87,23 @@ def _stream(dev) -> int:
 def _placed(fn):
     """Run a call on its first tensor's device and, when given, on `stream`:
     kernels, allocations and frees then all belong to that stream."""
+    sig = inspect.signature(fn)
+    name = next(iter(sig.parameters))
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         t = first.codes if isinstance(first, (PreparedInt8, WeightInt8)) else first
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{fn.__name__} needs CUDA tensors")
         if stream is None and t.device.index == torch._C._cuda_getDevice():
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
         if stream is not None and stream.device != t.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
         with torch.cuda.device(t.device), torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
+    call.__signature__ = sig.replace(parameters=[*sig.parameters.values(), inspect.Parameter(
+        "stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return call
 
 
@@ -371,9 +378,9 @@ def linear_int8(x: PreparedInt8, w: WeightInt8, bias=None, out_fp32: bool = Fals
     """Linear in 8-bit integers: Y[i, j] = x.scales[i] * w.scales[j] *
     sum_k x.codes[i, k] * w.codes[j, k] (+ bias[j]), the sum exact.  bias: bf16
     or fp32 [N]; Y: bf16, or fp32 with out_fp32."""
+    if not isinstance(x, PreparedInt8) or not isinstance(w, WeightInt8):
+        raise ValueError("linear_int8 takes a PreparedInt8 and a WeightInt8")
     dev = x.codes.device
-    if not isinstance(w, WeightInt8):
-        raise ValueError("w must be a WeightInt8")
     if w.K != x.K:
         raise ValueError(f"weight K={w.K} does not match the activations' K={x.K}")
     if not 16 <= x.K <= 65536 or x.K % 16:

@@ -169,3 +169,29 @@ def _aliased(dev):
     wide = torch.zeros((4, 128), dtype=torch.bfloat16, device=dev)
     x = wide[:, :64]
     return x, x.clone(), "rms", None, None, 1.0, None, None, None, None, 1e-6, False, wide.view(-1)[:256].view(4, 64)
+
+
+def test_first_argument_by_keyword_and_signature():
+    import inspect
+    z = torch.zeros((4, 8))
+    for call in (lambda: sq.moe_route(logits=z, k=2), lambda: sq.residual_norm(h=z, x=z), lambda: sq.prepare_int8(X=z),
+                 lambda: sq.linear_int8(w=None, x=sq.PreparedInt8(z, z, 4, 8)), lambda: sq.moe_route()):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    assert "stream" in inspect.signature(sq.moe_combine).parameters
+
+
+@gpu
+def test_calls_by_keyword():
+    x = torch.randn((4, 64), device="cuda").bfloat16()
+    q, s = sq.prepare_int8(x), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    by_name = sq.prepare_int8(X=x, stream=s)
+    y = sq.residual_norm(h=x, x=x)[1]
+    torch.cuda.synchronize()
+    assert torch.equal(q.codes, by_name.codes) and torch.equal(q.scales, by_name.scales)
+    assert torch.equal(y, sq.residual_norm(x, x)[1])
+    w = sq.quantize_weight_int8(W=x)
+    assert torch.equal(sq.linear_int8(x=q, w=w), sq.linear_int8(q, w))
+    with pytest.raises(ValueError, match="PreparedInt8"):
+        sq.linear_int8(x, w)
