@@ -69,6 +69,7 @@ struct RouteLaunch {
     int group_whole;            // a group is a power-of-two number of whole lanes
     int group_shift;            // log2 of the lanes that share a group
     int vectors;                // rows can be loaded in vectors
+    int bias_vectors;           // the biases can be loaded in vectors
 };
 
 struct DispatchLaunch {
