@@ -132,3 +132,11 @@ def test_quantised_linear_end_to_end():
     hx, hw = 0.5001 * x.scales.double()[:, None], 0.5001 * w.scales.double()
     bound = hx * W.double().abs().sum(1) + X.double().abs().sum(1)[:, None] * hw + K * hx * hw
     assert bool(((y - want).abs() <= bound + 1e-5 * want.abs().max()).all())
+
+
+@pytest.mark.parametrize("M", [3, 40, 64])
+@pytest.mark.parametrize("N,K", [(130, 65536), (1024, 4096), (3584, 3584), (6144, 4096), (10240, 8192), (12288, 4096),
+                                 (5000, 1040), (37000, 2064)])
+def test_every_split_of_k(M, N, K):
+    x, w = operands(M + N, M, N, K, full=True)
+    check(x, w)

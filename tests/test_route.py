@@ -253,3 +253,21 @@ def test_combine_into_the_residual():
     want = sq.moe_combine(Y, pos, w, residual=res)
     got = sq.moe_combine(Y, pos, w, residual=res, out=res)
     assert got is res and torch.equal(got, want)
+
+
+@gpu
+@pytest.mark.parametrize("offset", [0, 1, 2, 4])
+@pytest.mark.parametrize("T,E,groups", [(5, 128, 1), (300, 256, 8), (70, 200, 1), (70, 100, 5), (66, 60, 4), (9, 512, 16),
+                                        (80, 510, 1)])
+def test_route_bias_of_any_alignment(T, E, groups, offset):
+    l = logits_of(T + E, T, E)
+    g = np.random.default_rng(offset)
+    room = torch.from_numpy(0.2 * g.standard_normal(E + 4).astype(np.float32))
+    room[offset + E // 2], room[offset + E - 1] = NEG, float("nan")
+    bias = room.cuda()[offset:offset + E]
+    assert bias.data_ptr() % 16 == offset * 4 % 16
+    kw = dict(score="sigmoid", groups=groups, topk_groups=max(1, groups // 2), group_score="top2")
+    r = sq.moe_route(l.cuda(), 4, bias=bias, **kw)
+    ids, w = ref.route(l.numpy(), 4, bias=bias.cpu().numpy(), **kw)
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    assert np.all(np.abs(r.weights.cpu().numpy() - w) <= 2.0 ** -17 * np.abs(w) + 1e-37)
