@@ -505,7 +505,8 @@ def moe_linear(x: Prepared, row_index, offsets, w: Weight, out_fp32: bool = Fals
                ws=None, T: Optional[int] = None, stream=None):
     """Grouped two-path linear.  row_index: int32 [T] device tensor (or None:
     dispatched row t is prepared row t); offsets: int32 [E+1] device tensor;
-    w: E stacked expert weights (Weight.empty(..., E=E))."""
+    w: E stacked expert weights (Weight.empty(..., E=E)).  Rows from
+    offsets[E] on, which dropped choices leave (moe_route), are zeros."""
     import torch
     L = load_sharq_ops()
     if T is None:
@@ -531,7 +532,7 @@ def moe_linear_swiglu(x: Prepared, row_index, offsets, w: Weight, out=None, amax
                       T: Optional[int] = None, stream=None):
     """Grouped gate+up linear with the SwiGLU epilogue over E stacked
     interleaved expert weights: returns (H bf16 [T, w.N/2] in dispatch order,
-    amax fp32 [1] = max |H|)."""
+    amax fp32 [1] = max |H|).  Rows of H from offsets[E] on are zeros."""
     import torch
     L = load_sharq_ops()
     if T is None:

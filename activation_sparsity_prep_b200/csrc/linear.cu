@@ -1286,14 +1286,17 @@ cudaError_t launch_linear_t(const LinearLaunch& p, cudaStream_t s, int sms) {
 // Gather: dispatched row t of expert e (offsets[e] <= t < offsets[e+1])
 // reads prepared row row_index[t] (or t) and is written to padded row
 // poff[e] + (t - offsets[e]) of the workspace operands: both code rows and
-// both rows of scale atoms (4-byte words of four scales).
+// both rows of scale atoms (4-byte words of four scales).  Rows from offsets[E]
+// on are no expert's: their rows of the output, y_bytes long, become zeros, as
+// a prepare of the output takes its tensor scales over all rows.
 template <int FMT>
 __global__ void __launch_bounds__(256)
 moe_gather_kernel(const uint8_t* __restrict__ bb_codes, const uint8_t* __restrict__ bb_scales,
                   const uint8_t* __restrict__ rs_codes, const uint8_t* __restrict__ rs_scales,
                   const int32_t* __restrict__ row_index, Sched sc, int K, int64_t T,
                   uint8_t* __restrict__ gb_codes, uint8_t* __restrict__ gb_scales,
-                  uint8_t* __restrict__ gr_codes, uint8_t* __restrict__ gr_scales) {
+                  uint8_t* __restrict__ gr_codes, uint8_t* __restrict__ gr_scales,
+                  uint8_t* __restrict__ Y, int64_t y_bytes) {
     __shared__ SchedSmem ssm;
     sched_prepare(sc, &ssm);
     __syncthreads();
@@ -1302,6 +1305,11 @@ moe_gather_kernel(const uint8_t* __restrict__ bb_codes, const uint8_t* __restric
     const int row_bytes = K / 2;
     const int words = sc.nsf / 4;
     for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += warps) {
+        if (t >= ssm.g.t.off[sc.E]) {
+            uint4* y = reinterpret_cast<uint4*>(Y + t * y_bytes);
+            for (int64_t i = lane; i < y_bytes / 16; i += 32) y[i] = make_uint4(0, 0, 0, 0);
+            continue;
+        }
         int lo = 0, hi = sc.E;                      // expert of row t
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -1349,7 +1357,8 @@ cudaError_t launch_moe_t(const LinearLaunch& p, cudaStream_t s, int sms) {
         moe_gather_kernel<FMT><<<std::max(1, gblocks), 256, 0, s>>>(
             static_cast<const uint8_t*>(p.bb_codes), static_cast<const uint8_t*>(p.bb_scales),
             static_cast<const uint8_t*>(p.rs_codes), static_cast<const uint8_t*>(p.rs_scales),
-            p.row_index, sc, p.K, p.T, gb_codes, gb_scales, gr_codes, gr_scales);
+            p.row_index, sc, p.K, p.T, gb_codes, gb_scales, gr_codes, gr_scales, static_cast<uint8_t*>(p.Y),
+            p.swiglu ? (int64_t)p.N : (int64_t)p.N * (p.y_fp32 ? 4 : 2));
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

@@ -243,7 +243,8 @@ SHARQ_API sharq_status sharq_prepare_amax(const void* X_bf16, const float* amax,
  * expert_offsets is a DEVICE int32 array [E+1], offsets[0] = 0, offsets[E]
  * <= T, non-decreasing; row_index is a DEVICE int32 array [T] of rows < x->M.
  * Rows from offsets[E] on (dropped choices, see sharq_moe_dispatch) belong to
- * no expert: their row_index entries are read, their rows of Y not written.
+ * no expert: their row_index entries are not read, their rows of Y are zeros,
+ * so that a prepare of Y, whose tensor scales span all rows, may follow.
  * w holds E stacked weights (see sharq_weight), 1 <= E <= 256.  The
  * activation tensor scales are those of the whole prepare call.  Y is [T, N]
  * in dispatch order.  The call first gathers each expert's rows into ws
@@ -262,7 +263,8 @@ SHARQ_API sharq_status sharq_moe_linear(const sharq_prepared* x, const int32_t* 
  * for sharq_linear_swiglu (w holds E stacked [2I, K] weights, w->N = 2I), and
  * row t of H is silu(gate) * up of dispatched row t through its own expert's
  * weight, with the column pairing of sharq_linear_swiglu; H is bf16 [T, I]
- * in dispatch order, the down projection's input in that order.
+ * in dispatch order, the down projection's input in that order, with zeros in
+ * the rows of no expert.
  * *h_amax = max |H| over all T rows (0 for T = 0).  Arguments, workspace
  * and errors as sharq_moe_linear; NULL h_amax is SHARQ_ERR_INVALID_ARG. */
 SHARQ_API sharq_status sharq_moe_linear_swiglu(const sharq_prepared* x, const int32_t* row_index,
@@ -381,9 +383,8 @@ SHARQ_API sharq_status sharq_moe_route(const void* logits, int64_t ld, int logit
  * Writes row_index, offsets and position, which sharq_moe_linear and
  * sharq_moe_combine take.  An id outside 0 .. E-1 is dropped: its position
  * is -1 and it takes no row, so offsets[E] counts the live rows; row_index
- * entries from there on are 0, and the grouped linears leave those rows of
- * their output as they were (zero them where a prepare follows: its tensor
- * scales span all rows).  1 <= E <= 512, T * k < 2^31. */
+ * entries from there on are 0, and the grouped linears write zeros to those
+ * rows of their output.  1 <= E <= 512, T * k < 2^31. */
 SHARQ_API sharq_status sharq_moe_dispatch(const sharq_routing* r, void* stream);
 
 /* Expert outputs back to the tokens:
