@@ -120,6 +120,38 @@ __device__ __forceinline__ bool load_bias(const RouteLaunch& a, int lane, float 
     return __any_sync(kFull, masks);
 }
 
+// Largest value over the warp.
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Makes `top` the group's score, the sum of its two largest where top2 is set,
+// and returns the larger magnitude of its terms.
+template <typename F>
+__device__ __forceinline__ float group_sum(int top2, F& top, F second) {
+    float size = fabsf((float)top);
+    if (top2 && second > F(kNegInf)) {
+        size = fmaxf(size, fabsf((float)second));
+        top += second;
+    }
+    return size;
+}
+
+// Whether fp32 cannot tell the kept groups from those left behind: some lane's
+// kept group comes within the errors of another's that is not.  A group's score
+// is off by up to rel for each of its two scores of at most 1 and by 2^-24 of the
+// terms for each of their roundings and of the sum's, so the error follows the
+// terms, which can be far larger than a sum that cancels; twice that is allowed.
+// A sum past the range of fp32 is no score (-inf would drop the group).
+__device__ __forceinline__ bool groups_close(float score, float size, bool kept, float rel) {
+    const float err = 2.0f * (2.0f * rel + 2.4e-7f * (1.0f + size));
+    const float low = -redux_max(kept ? err - score : kNegInf);
+    const float high = redux_max(!kept && score > kNegInf ? score + err : kNegInf);
+    return low <= high || __any_sync(kFull, size < -kNegInf && !(fabsf(score) < -kNegInf));
+}
+
 // The choice for one token by one warp, a search round for each expert.
 // F = float returns false when two scores that the choice compares lie within
 // the error of their fp32 evaluation, or the chosen scores' sum underflows;
@@ -184,23 +216,20 @@ __device__ bool choose(const RouteLaunch& a, int64_t t, int lane, F* scratch) {
                 if (v > top) { second = top; top = v; }
                 else if (v > second) second = v;
             }
-            if (a.group_top2 && second > F(kNegInf)) top += second;
         }
+        const float size = group_sum(a.group_top2, top, second);
+        const F own = top;
         uint32_t chosen = 0;
-        F last = 0;
-        for (int r = 0; r <= a.topk_groups && r < a.groups; ++r) {
+        for (int r = 0; r < a.topk_groups && r < a.groups; ++r) {
             F v = top;
             int g = lane;
             warp_argmax(v, g);
             if (!(v > F(kNegInf))) break;
-            if (r == a.topk_groups) {
-                if (kFp32 && by_score && last - v <= F(4.0f * (2.0f * rel + 2.4e-7f * (1.0f + fabsf((float)last)))))
-                    return false;
-                break;
-            }
             chosen |= 1u << g;
-            last = v;
             if (lane == g) top = F(kNegInf);
+        }
+        if constexpr (kFp32) {
+            if (by_score && groups_close(own, size, chosen >> lane & 1u, rel)) return false;
         }
 #pragma unroll
         for (int j = 0; j < NPL; ++j)
@@ -247,13 +276,6 @@ struct RouteScratch {
     double key[36];                      // floats in the fp32 form; padded to a multiple of four
     int expert[32];
 };
-
-// Largest value over the warp.
-__device__ __forceinline__ float redux_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
 
 __device__ __forceinline__ float fast_exp(float v) {           // ex2.approx: 2^-22 + |v| 2^-23 relative
     float r;
@@ -323,7 +345,7 @@ __device__ __forceinline__ bool keep_groups(const F (&of)[NPL], F (&key)[NPL], c
         second = larger(smaller(top, t), larger(second, u));
         top = larger(top, t);
     }
-    if (a.group_top2 && second > F(kNegInf)) top += second;
+    const float size = group_sum(a.group_top2, top, second);
     if (g >= a.groups) top = F(kNegInf);
     // the groups not under the topk_groups-th largest score; where equal scores
     // make them too many, by rank with the lower index first
@@ -336,10 +358,7 @@ __device__ __forceinline__ bool keep_groups(const F (&of)[NPL], F (&key)[NPL], c
             if (left == bound) left = kNegInf;
         }
         kept = live && top >= bound;
-        if (inexact) {
-            const float best = redux_max(live && !kept ? top : kNegInf);
-            if (bound - best <= 4.0f * (2.0f * rel + 2.4e-7f * (1.0f + fabsf(bound)))) return false;
-        }
+        if (inexact && groups_close(top, size, kept, rel)) return false;
         if (__popc(__ballot_sync(kFull, kept)) > a.topk_groups << a.group_shift) {
             if (inexact) return false;
             const int rank = group_rank(top, g, a);       // a warp step: outside any lane's condition
