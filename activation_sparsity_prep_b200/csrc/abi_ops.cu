@@ -112,7 +112,7 @@ sharq_status sharq_residual_norm(const sharq_residual_norm_args* a, void* stream
         return SHARQ_ERR_INVALID_ARG;
     if (a->norm < SHARQ_NORM_NONE || a->norm > SHARQ_NORM_LAYER) return SHARQ_ERR_INVALID_ARG;
     if (a->M > 0 && !a->x) return SHARQ_ERR_INVALID_ARG;
-    if (!a->h && (a->post_gamma || a->gate)) return SHARQ_ERR_INVALID_ARG;
+    if (a->M > 0 && !a->h && (a->post_gamma || a->gate)) return SHARQ_ERR_INVALID_ARG;
     if (a->norm == SHARQ_NORM_NONE && (a->gamma || a->beta || a->scale || a->shift)) return SHARQ_ERR_INVALID_ARG;
     if (a->G < 1 || (a->M > 0 && a->M % a->G != 0)) return SHARQ_ERR_INVALID_ARG;
     const int xs = a->x_is_fp32 ? 4 : 2, hs = a->h_is_fp32 ? 4 : 2, ms = a->mod_is_fp32 ? 4 : 2;
