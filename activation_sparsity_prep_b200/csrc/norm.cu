@@ -96,7 +96,8 @@ __device__ __forceinline__ void fetch(const NormLaunch& a, int64_t row, uint8_t*
                   row_bytes(a) - x_bytes(a), bar);
 }
 
-// The row's 8-bit codes and scale.
+// The row's 8-bit codes and scale.  NaN and infinities reach the scale, so that
+// a product with the row is not finite either.
 template <int V>
 __device__ __forceinline__ void write_codes(const NormLaunch& a, int64_t row, const f2 (&t)[V][4], float (&red)[2][32],
                                             int& turn) {
@@ -107,11 +108,11 @@ __device__ __forceinline__ void write_codes(const NormLaunch& a, int64_t row, co
         for (int j = 0; j < 4; ++j) {
             float lo, hi;
             split_f2(t[i][j], lo, hi);
-            m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));
+            m = max_nan(m, max_nan(fabsf(lo), fabsf(hi)));
         }
     m = block_reduce<true>(m, red, turn);
     // below 2^-100 the reciprocal could overflow: such a row is zero
-    const bool live = m >= 7.8886091e-31f;
+    const bool live = !(m < 7.8886091e-31f);
     const float inv = live ? __fdiv_rn(127.0f, m) : 0.0f;
     if (threadIdx.x == 0) a.row_scale[row] = live ? __fdiv_rn(m, 127.0f) : 0.0f;
     int8_t* out = a.codes + row * a.K;

@@ -140,6 +140,19 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+// The larger value, NaN where one of them is (fmaxf would take the other).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
 // Bounded wait: a few hundred tries, each of which suspends the thread by
 // itself, then mbar_wait(), which times them by the global timer.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
@@ -149,12 +162,12 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
     return mbar_wait(bar, parity);
 }
 
-// Sum (or maximum) over the block, returned to every thread.  `red` holds
+// Sum (or maximum, NaN if any is) over the block, returned to every thread.  `red` holds
 // two sets of 32 words; successive calls alternate between them, so one
 // block barrier a call is enough.
 template <bool MAX>
 __device__ __forceinline__ float block_reduce(float v, float (&red)[2][32], int& turn) {
-    v = MAX ? warp_max(v) : warp_sum(v);
+    v = MAX ? warp_max_nan(v) : warp_sum(v);
     const int nw = blockDim.x >> 5;
     if (nw == 1) return v;
     float* r = red[turn & 1];
@@ -163,7 +176,7 @@ __device__ __forceinline__ float block_reduce(float v, float (&red)[2][32], int&
     __syncthreads();
     const int lane = threadIdx.x & 31;
     v = lane < nw ? r[lane] : 0.0f;      // zero is the identity of both (maxima are of magnitudes)
-    return MAX ? warp_max(v) : warp_sum(v);
+    return MAX ? warp_max_nan(v) : warp_sum(v);
 }
 
 }  // namespace sharq

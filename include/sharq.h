@@ -424,8 +424,9 @@ typedef struct {
  * (any may be NULL): out_x in x's type, y as bf16 [M, K], and q, y in 8 bits:
  *   a = max |y| of the row, scales = a / 127, codes = rne(y * (127 / a)),
  * the two quotients and the product each rounded to fp32; a row with
- * a < 2^-100 gets scale 0 and zero codes.  out_x may be x, or h when their
- * types agree.  gate, scale and shift are [G, K]: row r uses row
+ * a < 2^-100 gets scale 0 and zero codes; a row with a NaN or an infinity gets
+ * a scale that is not finite and codes without a meaning.  out_x may be x, or
+ * h when their types agree.  gate, scale and shift are [G, K]: row r uses row
  * r / (M / G); G divides M.  The vectors of a norm (post_gamma, gamma, beta)
  * share one type, those of the modulation (gate, scale, shift) another,
  * each bf16 or fp32; norm vectors and modulation need a norm, except gate.
