@@ -154,7 +154,7 @@ __device__ __forceinline__ bool groups_close(float score, float size, bool kept,
 
 // The choice for one token by one warp, a search round for each expert.
 // F = float returns false when two scores that the choice compares lie within
-// the error of their fp32 evaluation, or the chosen scores' sum underflows;
+// the error of their fp32 evaluation, or a chosen score is about to underflow;
 // the caller then repeats it in double, so that the experts are those of the
 // formula and not of its rounding.  Without a bias the scores' order is that
 // of the logits, which needs no evaluation.
@@ -261,7 +261,7 @@ __device__ bool choose(const RouteLaunch& a, int64_t t, int lane, F* scratch) {
     }
     if (a.renormalize) {
         const F sum = warp_sum(w);
-        if (kFp32 && sum < F(1e-30f) && __any_sync(kFull, id >= 0)) return false;
+        if (kFp32 && __any_sync(kFull, id >= 0 && w < F(1e-30f))) return false;
         w = sum > F(0) ? w / sum : F(0);
     }
     if (lane < a.k) {
@@ -574,7 +574,7 @@ __device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, i
     F w = chosen ? score : F(0);
     if (a.renormalize) {
         const F sum = warp_sum(w);
-        if (kFp32 && sum < F(1e-30f) && count > 0) return kTooClose;
+        if (kFp32 && a.sigmoid && __any_sync(kFull, chosen && w < F(1e-30f))) return kTooClose;
         w = sum > F(0) ? quotient(w, sum) : F(0);
     }
     const int64_t to = t * a.k;
