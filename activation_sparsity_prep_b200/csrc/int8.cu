@@ -9,9 +9,10 @@
 // Three forms:
 //   dot     one or two tokens: a warp for two or four channels on the
 //           dot-product units, bound by streaming the weight;
-//   swapped up to 64 tokens (128 in narrow, long layers): 128 channels x all tokens on the tensor cores
-//           (the weight is the M-side operand), K split over a cluster so
-//           that narrow layers use every SM; bound by the weight;
+//   swapped up to 64 tokens (128 in narrow, long layers): 128 channels x all
+//           tokens on the tensor cores (the weight is the M-side operand), K
+//           split over a cluster so that narrow layers use every SM; bound by
+//           the weight;
 //   tiled   128 or 256 tokens x up to 256 channels a tile, persistent, bound
 //           by the tensor cores.
 #include <cuda.h>
@@ -767,8 +768,11 @@ cudaError_t launch_linear_int8(const Int8Launch& p, cudaStream_t s, int sms) {
         return p.M == 1 ? launch_dot<1>(p, s) : launch_dot<2>(p, s);
     // Up to 64 tokens, unless K is short: nothing to split, and the tiled form
     // has less to set up (48 x 1024 x 1024: 4.5 against 5.9 us).  Up to 128 where
-    // K is long and there are too few channels for tiles on every SM (128 x 4096
-    // x 14336: 18.1 against 20.3 us).
+    // K is long and there are too few channels for tiles on every SM (N x K, tiled
+    // against swapped, us; 72 tokens: 4096 x 14336 19.4 and 15.8, 4736 x 14336 20.5
+    // and 18.8, 8192 x 14336 26.3 and 30.2, 4096 x 4096 8.9 and 8.2; 128 tokens:
+    // 19.5 and 18.4, 20.4 and 22.2, 26.8 and 35.0, 8.9 and 9.9; 4096 x 8192: 13.1 and
+    // 11.4 for 72, 13.1 and 13.2 for 128).
     if (p.K > 1024 && p.M <= (p.K >= 8192 && p.N <= 64 * sms / 2 ? kSwappedTokens : 64)) return launch_swapped(p, s, sms);
     return launch_tiled(p, s, sms);
 }

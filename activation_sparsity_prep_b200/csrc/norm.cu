@@ -605,9 +605,12 @@ cudaError_t launch_residual_norm(const NormLaunch& p, cudaStream_t s, int sms) {
     // At most 512 threads; the split of a row depends on K and on the parts of
     // the call, not on M.  Four chunks a thread halve what a row's reductions
     // and flags cost a warp, and pay where that counts: the bf16 quantiser and
-    // two norms (4096 x 3584: 11.7 -> 8.4 us, 22.6 -> 20.5 us); with one
+    // two norms (4096 x 3584: 12.2 -> 9.9 us, 22.6 -> 21.4 us); with one
     // reduction and more bytes two chunks keep more warps resident (8190 x
-    // 5120 fp32: 84 against 94 us).
+    // 5120 fp32: 84 against 94 us).  The bound is where a norm into 8 bits
+    // crosses (4096 rows, two chunks against four: K = 2816 14.4 and 17.9 us,
+    // 3200 16.1 and 16.0, 4096 19.0 and 17.3); the quantiser alone and two norms
+    // gain from 1024 on, by a tenth (2560: 8.9 and 8.6, 18.2 and 17.2).
     const bool long_work = p.K > 3200 && !p.x_fp32 && (!p.h || p.post_gamma);
     if (p.K <= 256) return launch_x<1>(p, s, sms);
     if (p.K <= 8192 && !long_work) return launch_x<2>(p, s, sms);

@@ -423,9 +423,9 @@ __device__ __noinline__ int exact_rank(const RouteLaunch* a, int64_t t, int lane
 // The choice without a search round for each expert.  The k-th largest of the
 // 32 lane maxima bounds the k-th largest key from below, so the few keys not
 // under it are gathered, in expert order, and ranked against one another.
-// The kernel is bound by instruction issue: 16383 tokens of 256 experts, sigmoid
-// with bias, took 13.8 M warp instructions and 30 us with search rounds, and
-// take 12.6 us so.  F = float ranks close candidates in double, and
+// What a token costs is instructions, not memory (issue slots 71 % busy, DRAM 9 %):
+// 16383 tokens of 256 experts, sigmoid with bias, took 13.8 M warp instructions
+// and 30 us with search rounds, and take 12.6 us so.  F = float ranks close candidates in double, and
 // leaves close groups and underflow to F = double (kTooClose), which gathers on
 // its keys rounded to fp32, an order-preserving step, and ranks the keys
 // themselves.  Nothing is written unless kChosen is returned.
@@ -630,7 +630,7 @@ route_kernel(const __grid_constant__ RouteLaunch a) {
 // memory; the rows are scanned over the block's warps, the block totals over
 // the cluster (distributed shared memory) and the experts, and a second walk
 // over the same run places each choice.  Equal ids inside a group of 32 are
-// ranked by a warp match, so the order is fixed; no workspace.
+// ranked by ballots, so the order is fixed; no workspace.
 constexpr int kDispWarps = 32;
 constexpr int kBatch = 8;            // groups of 32 choices whose loads are in flight together
 constexpr int kHeld = 2;             // groups of a run short enough to stay in registers

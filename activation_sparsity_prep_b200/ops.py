@@ -197,8 +197,10 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     is masked; score: "softmax" or "sigmoid"; bias: fp32 [E], added for the
     choice only; groups / topk_groups / group_score ("max" or "top2"): keep
     the best groups of neighbouring experts first.  A token with fewer than k
-    experts left has ids of -1 and weights of 0 behind them.  The result's
-    row_index and offsets go to moe_linear, position and weights to
+    experts left has ids of -1 and weights of 0 behind them; those choices take
+    no dispatched row, and the grouped linears return zeros in the rows behind
+    the last live one.  The result's row_index and offsets go to moe_linear (up
+    to 256 experts, where E may be 512 here), position and weights to
     moe_combine."""
     if logits.dim() != 2:
         raise ValueError("logits must be a 2-D tensor [T, E]")
@@ -332,7 +334,9 @@ def _check_extent(K: int) -> None:
 @_placed
 def prepare_int8(X, gamma=None, eps: float = 1e-6, out: Optional[PreparedInt8] = None) -> PreparedInt8:
     """X bf16 [M, K] -> 8-bit codes and a scale for each row, after RMSNorm
-    with gamma (bf16 [K]) when it is given."""
+    with gamma (bf16 [K]) when it is given.  K: a multiple of 8 up to 32768
+    (of 16 where linear_int8 follows).  A row with NaN or infinities gets a
+    scale that is not finite."""
     if X.dim() != 2:
         raise ValueError("X must be a 2-D tensor [M, K]")
     M, K = X.shape
@@ -354,7 +358,8 @@ def prepare_int8(X, gamma=None, eps: float = 1e-6, out: Optional[PreparedInt8] =
 
 @_placed
 def quantize_weight_int8(W, out: Optional[WeightInt8] = None) -> WeightInt8:
-    """W bf16 [N, K] -> 8-bit codes and a scale for each output channel."""
+    """W bf16 [N, K] -> 8-bit codes and a scale for each output channel; K as
+    prepare_int8."""
     if W.dim() != 2:
         raise ValueError("W must be a 2-D tensor [N, K]")
     N, K = W.shape
@@ -376,8 +381,9 @@ def quantize_weight_int8(W, out: Optional[WeightInt8] = None) -> WeightInt8:
 @_placed
 def linear_int8(x: PreparedInt8, w: WeightInt8, bias=None, out_fp32: bool = False, out=None):
     """Linear in 8-bit integers: Y[i, j] = x.scales[i] * w.scales[j] *
-    sum_k x.codes[i, k] * w.codes[j, k] (+ bias[j]), the sum exact.  bias: bf16
-    or fp32 [N]; Y: bf16, or fp32 with out_fp32."""
+    sum_k x.codes[i, k] * w.codes[j, k] (+ bias[j]), the sum exact.  K: a
+    multiple of 16 up to 65536; bias: bf16 or fp32 [N]; Y: bf16, or fp32 with
+    out_fp32."""
     if not isinstance(x, PreparedInt8) or not isinstance(w, WeightInt8):
         raise ValueError("linear_int8 takes a PreparedInt8 and a WeightInt8")
     dev = x.codes.device

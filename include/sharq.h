@@ -368,12 +368,15 @@ typedef struct {
  *   weights: s (without the bias) of each, divided by their sum when
  *   renormalize is set (0 when that sum is 0), times scale.
  * The comparisons decide as they would in 64-bit arithmetic: scores that
- * fp32 cannot tell apart are evaluated again in double.  A softmax over a
+ * fp32 cannot tell apart are evaluated again in double.  Without a bias the
+ * scores of experts, and the largest of a group, compare as their logits do,
+ * also where their 64-bit values would round alike.  A softmax over a
  * logit of +inf has no value: that token's ids (in -1 .. E-1) and weights are
  * unspecified.
  * 1 <= E <= 512, E a multiple of groups, 1 <= k <= 32, k at most the experts
- * of topk_groups groups, T * k < 2^31.  When out->row_index is not NULL the
- * dispatch order is built too, as sharq_moe_dispatch. */
+ * of topk_groups groups, T * k < 2^31; the grouped linears take at most 256
+ * experts.  When out->row_index is not NULL the dispatch order is built too,
+ * as sharq_moe_dispatch. */
 SHARQ_API sharq_status sharq_moe_route(const void* logits, int64_t ld, int logits_fp32,
                                        const float* bias, const sharq_route_options* opt,
                                        const sharq_routing* out, void* stream);
@@ -457,7 +460,8 @@ SHARQ_API sharq_status sharq_residual_norm(const sharq_residual_norm_args* a, vo
 
 /* 8-bit operand of a linear, beside sharq_prepare: X bf16 [M, K], RMSNorm
  * with gamma bf16 [K] in front (NULL: none), codes and scales as
- * sharq_residual_norm's q.  Extents as there. */
+ * sharq_residual_norm's q.  Extents as there (sharq_linear_int8 also wants
+ * K % 16 == 0; longer rows than these it takes as codes made elsewhere). */
 SHARQ_API sharq_status sharq_prepare_int8(const void* X_bf16, const void* gamma_bf16, float eps,
                                           const sharq_prepared_int8* out, void* stream);
 
