@@ -1304,12 +1304,9 @@ moe_gather_kernel(const uint8_t* __restrict__ bb_codes, const uint8_t* __restric
     const int64_t warps = (int64_t)gridDim.x * 8;
     const int row_bytes = K / 2;
     const int words = sc.nsf / 4;
-    for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += warps) {
-        if (t >= ssm.g.t.off[sc.E]) {
-            uint4* y = reinterpret_cast<uint4*>(Y + t * y_bytes);
-            for (int64_t i = lane; i < y_bytes / 16; i += 32) y[i] = make_uint4(0, 0, 0, 0);
-            continue;
-        }
+    const int64_t live = min(T, (int64_t)ssm.g.t.off[sc.E]);
+    int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    for (; t < live; t += warps) {
         int lo = 0, hi = sc.E;                      // expert of row t
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -1330,6 +1327,10 @@ moe_gather_kernel(const uint8_t* __restrict__ bb_codes, const uint8_t* __restric
             *reinterpret_cast<uint32_t*>(gr_scales + d0 + w * 512) =
                 *reinterpret_cast<const uint32_t*>(rs_scales + so + w * 512);
         }
+    }
+    for (; t < T; t += warps) {
+        uint4* y = reinterpret_cast<uint4*>(Y + t * y_bytes);
+        for (int64_t i = lane; i < y_bytes / 16; i += 32) y[i] = make_uint4(0, 0, 0, 0);
     }
 }
 
