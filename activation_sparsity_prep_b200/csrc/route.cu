@@ -425,10 +425,11 @@ __device__ __noinline__ int exact_rank(const RouteLaunch* a, int64_t t, int lane
 // under it are gathered, in expert order, and ranked against one another.
 // What a token costs is instructions, not memory (issue slots 71 % busy, DRAM 9 %):
 // 16383 tokens of 256 experts, sigmoid with bias, took 13.8 M warp instructions
-// and 30 us with search rounds, and take 12.6 us so.  F = float ranks close candidates in double, and
-// leaves close groups and underflow to F = double (kTooClose), which gathers on
-// its keys rounded to fp32, an order-preserving step, and ranks the keys
-// themselves.  Nothing is written unless kChosen is returned.
+// and 30 us with search rounds, and take 12.6 us so.  F = float ranks close
+// candidates in double, and leaves close groups and scores about to underflow to
+// F = double (kTooClose), which gathers on its keys rounded to fp32, an
+// order-preserving step, and ranks the keys themselves.  Nothing is written
+// unless kChosen is returned.
 template <int NPL, bool SCORED, bool GROUPS, typename F>
 __device__ __forceinline__ Choice choose_fast(const RouteLaunch& a, int64_t t, int lane, const float (&b)[NPL],
                                               bool bias_masks, F* scratch, RouteScratch& sh) {
